@@ -24,12 +24,18 @@ MODE_TOPK, MODE_OEA = 0, 1
 DTYPE_BF16, DTYPE_F32 = 0, 1
 FLAG_NONFINITE_SCORE, FLAG_WAIT_TIMEOUT, FLAG_BAD_INDEX = 0x1, 0x2, 0x4
 MAX_TOKENS, MAX_EXPERTS, MAX_SLOTS = 256, 1024, 32
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+MAX_GROUPS, MAX_HEAD_DIM, MAX_PAGE, MAX_REQUESTS = 32, 256, 65536, 1024
+ATTENTION_WORKSPACE_MIN = 512
 
 EXPORTED = ["moe_num_slots", "moe_layer_launches", "moe_workspace_bytes", "moe_route", "moe_expert_ffn",
             "moe_expert_ffn_mixed", "moe_pack_int4", "moe_decode_layer", "moe_decode_layer_mixed", "moe_decode_layer_static",
             "moe_device_status", "moe_device_status_static", "moe_set_wait_timeout_us",
             "moe_residency_create", "moe_residency_observe", "moe_residency_flush", "moe_residency_query",
-            "moe_residency_destroy", "moe_residency_select", "moe_synth_normal", "moe_status_string", "moe_last_error"]
+            "moe_residency_destroy", "moe_residency_select", "moe_synth_normal", "moe_status_string", "moe_last_error",
+            "moe_route_scores", "moe_route_grouped", "moe_decode_layer_grouped", "moe_rope_table", "moe_kv_append",
+            "moe_attention_workspace_bytes", "moe_tree_attention"]
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -63,6 +69,33 @@ class _Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("expert_idx", "weights", "T", "active", "counts", "offsets", "perm",
                  "n_base", "logits")]
+
+
+class _Select(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "page_table")] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "kv_heads", "head_dim", "n_requests", "max_pages",
+                                             "dtype")]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32)] + \
+               [(n, ctypes.c_double) for n in ("base", "factor", "original_len", "beta_fast", "beta_slow", "magnitude")]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "heads", "rot", "n_pos", "interleaved")] + \
+               [(n, ctypes.c_int64) for n in ("q_tok", "q_head", "k_tok", "k_head", "v_tok", "v_head", "out_tok",
+                                             "out_head")]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("heads", ctypes.c_int32), ("mask_words", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_tok", ctypes.c_int64), ("q_head", ctypes.c_int64)]
 
 
 _lib = None
@@ -101,6 +134,21 @@ def load(path: str | None = None):
     lib.moe_decode_layer_static.argtypes = [V, V, V, V, V, V, ctypes.c_int32, P(_Params), P(_Routing),
                                             V, V]
     lib.moe_decode_layer_static.restype = ctypes.c_int
+    lib.moe_route_scores.argtypes = [V, V, V, V, V, V, ctypes.c_size_t, V]
+    lib.moe_route_scores.restype = ctypes.c_int
+    lib.moe_route_grouped.argtypes = [V, V, V, V, P(_Params), P(_Select), P(_Routing), V, ctypes.c_size_t, V]
+    lib.moe_route_grouped.restype = ctypes.c_int
+    lib.moe_decode_layer_grouped.argtypes = [V, V, V, V, V, V, V, ctypes.c_int32, P(_Params), P(_Select), P(_Routing),
+                                             V, V, ctypes.c_size_t, V]
+    lib.moe_decode_layer_grouped.restype = ctypes.c_int
+    lib.moe_rope_table.argtypes = [P(_Rope), ctypes.c_int32, V, V]
+    lib.moe_rope_table.restype = ctypes.c_int
+    lib.moe_kv_append.argtypes = [V, V, V, V, V, V, V, V, V, V, ctypes.c_size_t, V]
+    lib.moe_kv_append.restype = ctypes.c_int
+    lib.moe_attention_workspace_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32, P(_KvCache)]
+    lib.moe_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_tree_attention.argtypes = [V, V, V, V, V, V, V, V, V, ctypes.c_size_t, V]
+    lib.moe_tree_attention.restype = ctypes.c_int
     lib.moe_device_status.argtypes = [V, V, P(ctypes.c_uint32)]
     lib.moe_device_status.restype = ctypes.c_int
     lib.moe_device_status_static.argtypes = [V, P(ctypes.c_uint32)]
@@ -454,6 +502,244 @@ def moe_decode_layer_static(hidden, w_router, router_bias, w_gate, w_up, w_down,
                                         _ptr(w_up), _ptr(w_down), d_ff, ctypes.byref(params.c()),
                                         ctypes.byref(routing.c()), _ptr(out), _stream(stream))
     _check(st, "moe_decode_layer_static")
+    return out
+
+
+@dataclasses.dataclass
+class SelectParams:
+    """Mirror of moe_select_params (include/moe.h)."""
+    score: int = SCORE_SOFTMAX
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalise: bool = True
+    scale: float = 1.0
+
+    def c(self) -> _Select:
+        return _Select(self.score, self.n_group, self.topk_group, self.group_top, int(self.renormalise), self.scale)
+
+
+def moe_route_scores(scores, select_bias, params: RouteParams, select: SelectParams, routing: Routing,
+                     workspace: torch.Tensor, stream=None):
+    """Selection and grouping of given router scores ([B][N] fp32)."""
+    _need(scores, torch.float32, "scores")
+    if scores.shape != (params.B, params.N):
+        raise ValueError(f"scores must be [{params.B}][{params.N}]")
+    _need_bias(select_bias, params.N)
+    st = load().moe_route_scores(_ptr(scores), _ptr(select_bias), ctypes.byref(params.c()), ctypes.byref(select.c()),
+                                 ctypes.byref(routing.c()), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "moe_route_scores")
+    return routing
+
+
+def _need_bias(select_bias, N):
+    if select_bias is not None:
+        _need(select_bias, torch.float32, "select_bias")
+        if select_bias.numel() != N:
+            raise ValueError(f"select_bias must hold {N} values")
+
+
+def moe_route_grouped(hidden, w_router, router_bias, select_bias, params: RouteParams, select: SelectParams,
+                      routing: Routing, workspace: torch.Tensor, stream=None):
+    """moe_route with the selection of SelectParams."""
+    dt = params.torch_dtype
+    _need(hidden, dt, "hidden")
+    _need(w_router, dt, "w_router")
+    if router_bias is not None:
+        _need(router_bias, torch.float32, "router_bias")
+    _need_bias(select_bias, params.N)
+    st = load().moe_route_grouped(_ptr(hidden), _ptr(w_router), _ptr(router_bias), _ptr(select_bias),
+                                  ctypes.byref(params.c()), ctypes.byref(select.c()), ctypes.byref(routing.c()),
+                                  _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "moe_route_grouped")
+    return routing
+
+
+def moe_decode_layer_grouped(hidden, w_router, router_bias, select_bias, w_gate, w_up, w_down, d_ff: int,
+                             params: RouteParams, select: SelectParams, routing: Routing, out,
+                             workspace: torch.Tensor, stream=None):
+    """The whole layer with the selection of SelectParams."""
+    dt = params.torch_dtype
+    for t, n in ((hidden, "hidden"), (w_router, "w_router"), (w_gate, "w_gate"), (w_up, "w_up"),
+                 (w_down, "w_down"), (out, "out")):
+        _need(t, dt, n)
+    if router_bias is not None:
+        _need(router_bias, torch.float32, "router_bias")
+    _need_bias(select_bias, params.N)
+    st = load().moe_decode_layer_grouped(_ptr(hidden), _ptr(w_router), _ptr(router_bias), _ptr(select_bias),
+                                         _ptr(w_gate), _ptr(w_up), _ptr(w_down), d_ff, ctypes.byref(params.c()),
+                                         ctypes.byref(select.c()), ctypes.byref(routing.c()), _ptr(out),
+                                         _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "moe_decode_layer_grouped")
+    return out
+
+
+@dataclasses.dataclass
+class RopeParams:
+    """Mirror of moe_rope_params (include/moe.h)."""
+    rot: int
+    base: float = 10000.0
+    scaling: int = ROPE_PLAIN
+    factor: float = 1.0
+    original_len: float = 0.0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    magnitude: float = 0.0
+
+    def c(self) -> _Rope:
+        return _Rope(self.rot, self.scaling, self.base, self.factor, self.original_len, self.beta_fast, self.beta_slow,
+                     self.magnitude)
+
+
+def moe_rope_table(params: RopeParams, n_pos: int, device="cuda", out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The table of cosines and sines [n_pos][rot] that moe_kv_append reads."""
+    if out is None:
+        out = torch.empty(max(n_pos, 0), max(params.rot, 0), dtype=torch.float32, device=device)
+    _need(out, torch.float32, "out")
+    if out.shape != (n_pos, params.rot):
+        raise ValueError(f"out must be [{n_pos}][{params.rot}]")
+    _check(load().moe_rope_table(ctypes.byref(params.c()), n_pos, _ptr(out), _stream(stream)), "moe_rope_table")
+    return out
+
+
+class KvCache:
+    """moe_kv_cache: a paged cache over the caller's tensors.  k and v are
+    [n_pages][kv_heads][page_size][head_dim] (bf16 or fp32), page_table
+    [n_requests][max_pages] int32 (None for a cache that is only appended
+    to).  The tensors' contents may change between calls; the tensors
+    themselves stay for the life of this object."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor | None = None):
+        if k.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("k must be bf16 or fp32")
+        for t, n in ((k, "k"), (v, "v")):
+            _need(t, k.dtype, n)
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [n_pages][kv_heads][page_size][head_dim], of one shape")
+        if page_table is not None:
+            _need(page_table, torch.int32, "page_table")
+            if page_table.dim() != 2:
+                raise ValueError("page_table must be [n_requests][max_pages]")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.n_requests, self.max_pages = page_table.shape if page_table is not None else (0, 0)
+        self.dtype = k.dtype
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr() if page_table is not None else None,
+                           self.n_pages, self.page_size, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
+                           DTYPE_BF16 if k.dtype == torch.bfloat16 else DTYPE_F32)
+
+    def c(self) -> _KvCache:
+        return self._c
+
+
+def moe_attention_workspace_bytes(T: int, heads: int, cache: KvCache) -> int:
+    n = load().moe_attention_workspace_bytes(T, heads, ctypes.byref(cache.c()))
+    if n == 0:
+        raise MoeError(MOE_ERR_ARG, "moe_attention_workspace_bytes", load().moe_last_error().decode())
+    return n
+
+
+def alloc_attention_workspace(T: int, heads: int, cache: KvCache, device) -> torch.Tensor:
+    """A zero-filled workspace for moe_kv_append and moe_tree_attention of up
+    to T tokens with `heads` query heads on this cache."""
+    return torch.zeros(moe_attention_workspace_bytes(T, heads, cache), dtype=torch.uint8, device=device)
+
+
+def _need_heads(t, dtype, shape, name):
+    """A CUDA tensor [tokens][heads][head_dim] whose heads are dense inside."""
+    if t.dtype != dtype or not t.is_cuda or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA tensor {tuple(shape)} of {dtype}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: the components of a head must be adjacent")
+    return s
+
+
+def moe_kv_append(q, k, v, rope, positions, slots, cache: KvCache, q_out, workspace: torch.Tensor,
+                  interleaved: bool = False, stream=None):
+    """Rotates q (into q_out) and k, and writes k and v into the cache.
+    q and k/v: [T][heads][head_dim] and [T][kv_heads][head_dim], any distances
+    between tokens and heads that are multiples of 16 bytes; rope: the table
+    of moe_rope_table, or None (no rotation); q and q_out may both be None."""
+    T, D, dt = k.shape[0], cache.head_dim, cache.dtype
+    ks = _need_heads(k, dt, (T, cache.kv_heads, D), "k")
+    vs = _need_heads(v, dt, (T, cache.kv_heads, D), "v")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out must both be given, or neither")
+    heads, qs, os_ = 0, (0, 0), (0, 0)
+    if q is not None:
+        heads = q.shape[1]
+        qs = _need_heads(q, dt, (T, heads, D), "q")
+        os_ = _need_heads(q_out, dt, (T, heads, D), "q_out")
+    n_pos, rot = 0, 0
+    if rope is not None:
+        _need(rope, torch.float32, "rope")
+        n_pos, rot = rope.shape
+        _need(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError(f"positions must hold {T} values")
+    _need(slots, torch.int64, "slots")
+    if slots.numel() != T:
+        raise ValueError(f"slots must hold {T} values")
+    prm = _Append(T, heads, rot, n_pos, int(interleaved), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    st = load().moe_kv_append(_ptr(q), _ptr(k), _ptr(v), _ptr(rope), _ptr(positions), _ptr(slots), ctypes.byref(prm),
+                              ctypes.byref(cache.c()), _ptr(q_out), _ptr(workspace), workspace.numel(),
+                              _stream(stream))
+    _check(st, "moe_kv_append")
+    return q_out
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """Mask words (int32, CPU) of one request's drafted tree: parents[i] < i
+    is the drafted token that token i continues, or -1 for one that continues
+    the context.  Token i sees itself and its ancestors.  Host-side
+    arithmetic."""
+    rows = []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i:
+            raise ValueError(f"parents[{i}]={p} must be -1 or an earlier token")
+        rows.append((rows[p] if p >= 0 else 0) | 1 << i)
+    words = (len(rows) + 31) // 32
+    bits = [[(r >> (32 * w)) & 0xffffffff for w in range(words)] for r in rows]
+    return torch.tensor(bits, dtype=torch.int64).reshape(len(rows), words).to(torch.int32)
+
+
+def moe_tree_attention(q, q_offsets, ctx_len, mask, cache: KvCache, out, lse, workspace: torch.Tensor,
+                       scale: float | None = None, stream=None):
+    """Attention of the step's tokens q [T][heads][head_dim] to their requests'
+    caches: request r's tokens q_offsets[r]..q_offsets[r+1]-1 see its first
+    ctx_len[r] positions, and of the step's own tokens those that mask ([T]
+    [words] int32 bits) allows (None: the token itself and those before it).
+    scale: 1 / sqrt(head_dim) by default.  lse may be None."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T][heads][head_dim]")
+    T, heads = q.shape[0], q.shape[1]
+    D, dt = cache.head_dim, cache.dtype
+    qs = _need_heads(q, dt, (T, heads, D), "q")
+    _need(out, dt, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.shape != (T, heads):
+            raise ValueError(f"lse must be [{T}][{heads}]")
+    R = cache.n_requests
+    _need(q_offsets, torch.int32, "q_offsets")
+    _need(ctx_len, torch.int32, "ctx_len")
+    if q_offsets.numel() != R + 1 or ctx_len.numel() != R:
+        raise ValueError(f"q_offsets must hold {R + 1} values and ctx_len {R}")
+    words = 0
+    if mask is not None:
+        _need(mask, torch.int32, "mask")
+        if mask.dim() != 2 or mask.shape[0] != T:
+            raise ValueError(f"mask must be [{T}][words]")
+        words = mask.shape[1]
+    prm = _Attention(T, heads, words, D ** -0.5 if scale is None else scale, qs[0], qs[1])
+    st = load().moe_tree_attention(_ptr(q), _ptr(q_offsets), _ptr(ctx_len), _ptr(mask), ctypes.byref(prm),
+                                   ctypes.byref(cache.c()), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                   _stream(stream))
+    _check(st, "moe_tree_attention")
     return out
 
 

@@ -549,43 +549,52 @@ moe_status expert_ffn_impl(const void* hidden, const void* w_gate, const void* w
     }
 
 }
-}  // namespace
-
-extern "C" {
-
-int32_t moe_num_slots(const moe_route_params* params) {
-    Params P;
-    if (resolve(params, P) != MOE_OK) return -1;
-    return P.kslots;
+// moe_select_params checked against the routing parameters.
+moe_status resolve_select(const moe_select_params* in, const float* bias, const Params& P, SelectArgs& S) {
+    if (P.mode != MOE_MODE_TOPK) return fail(MOE_ERR_ARG, "this selection needs mode MOE_MODE_TOPK");
+    if (in->score != MOE_SCORE_SOFTMAX && in->score != MOE_SCORE_SIGMOID)
+        return fail(MOE_ERR_ARG, "unknown score %d", in->score);
+    if (in->n_group < 1 || in->n_group > MOE_MAX_GROUPS || P.N % in->n_group != 0)
+        return fail(MOE_ERR_ARG, "n_group=%d must divide N=%d and lie in 1..%d", in->n_group, P.N, MOE_MAX_GROUPS);
+    const int gs = P.N / in->n_group;
+    if (in->topk_group < 1 || in->topk_group > in->n_group)
+        return fail(MOE_ERR_ARG, "topk_group=%d outside 1..n_group=%d", in->topk_group, in->n_group);
+    if (in->group_top < 1 || in->group_top > 2 || in->group_top > gs)
+        return fail(MOE_ERR_ARG, "group_top=%d must be 1 or 2 and at most N / n_group=%d", in->group_top, gs);
+    if (P.k > in->topk_group * gs)
+        return fail(MOE_ERR_ARG, "k=%d is above the %d experts of %d groups", P.k, in->topk_group * gs, in->topk_group);
+    if (in->renormalise != 0 && in->renormalise != 1) return fail(MOE_ERR_ARG, "renormalise must be 0 or 1");
+    if (!std::isfinite(in->scale)) return fail(MOE_ERR_ARG, "scale is not finite");
+    if (!aligned(bias, 4)) return fail(MOE_ERR_ARG, "select_bias not 4-byte aligned");
+    S.bias = bias;
+    S.sigmoid = in->score == MOE_SCORE_SIGMOID;
+    // all groups stay: as without groups
+    S.n_group = in->topk_group == in->n_group ? 1 : in->n_group;
+    S.topk_group = in->topk_group;
+    S.group_top = S.n_group == 1 ? 1 : in->group_top;
+    S.renorm = in->renormalise;
+    S.scale = in->scale;
+    return MOE_OK;
 }
 
-int32_t moe_layer_launches(const moe_route_params* params, int32_t d_ff) {
-    Params P;
-    if (resolve(params, P) != MOE_OK) return -1;
-    if (d_ff <= 0 || d_ff % 64 != 0 || d_ff > 16384) return -1;
-    int32_t n = route_fused_supported(P.dtype, P.B, P.N, P.kslots) ? 1 : (P.B > 0 ? 2 : 1);
-    if (P.B > 0) n += P.dtype == MOE_DTYPE_F32 ? 3 : 1;
-    return n;
-}
-
-size_t moe_workspace_bytes(const moe_route_params* params, int32_t d_ff) {
-    Params P;
-    if (resolve(params, P) != MOE_OK) return 0;
-    if (d_ff < 0 || d_ff % 64 != 0 || d_ff > 16384) return 0;
-    const WsLayout L = layout(P, d_ff);
-    return d_ff == 0 ? L.hbuf : L.total;
-}
-
-moe_status moe_route(const void* hidden, const void* w_router, const float* router_bias,
-                     const moe_route_params* params, const moe_routing* routing, void* workspace,
-                     size_t workspace_bytes, moe_stream_t stream) {
+// Routing of the caller's scores, or of the router's (scores null), by the
+// plain rule or OEA (select null) or by moe_select_params.
+moe_status route_impl(const void* hidden, const void* w_router, const float* router_bias, const float* scores,
+                      const float* select_bias, const moe_route_params* params, const moe_select_params* select,
+                      const moe_routing* routing, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
     Params P;
     moe_status st = resolve(params, P);
     if (st != MOE_OK) return st;
     if ((st = check_routing(routing, true, P.B)) != MOE_OK) return st;
-    if ((!hidden && P.B > 0) || !w_router) return fail(MOE_ERR_ARG, "hidden or w_router is NULL");
-    if (!aligned(hidden, 16) || !aligned(w_router, 16)) return fail(MOE_ERR_ARG, "hidden/w_router not 16-byte aligned");
-    if (router_bias && !aligned(router_bias, 4)) return fail(MOE_ERR_ARG, "router_bias not 4-byte aligned");
+    SelectArgs sa{};
+    if (select && (st = resolve_select(select, select_bias, P, sa)) != MOE_OK) return st;
+    if (!scores) {
+        if ((!hidden && P.B > 0) || !w_router) return fail(MOE_ERR_ARG, "hidden or w_router is NULL");
+        if (!aligned(hidden, 16) || !aligned(w_router, 16)) return fail(MOE_ERR_ARG, "hidden/w_router not 16-byte aligned");
+        if (router_bias && !aligned(router_bias, 4)) return fail(MOE_ERR_ARG, "router_bias not 4-byte aligned");
+    } else if (!aligned(scores, 4)) {
+        return fail(MOE_ERR_ARG, "scores not 4-byte aligned");
+    }
     const WsLayout L = layout(P, 0);
     if ((st = check_ws(workspace, workspace_bytes, L.hbuf)) != MOE_OK) return st;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -600,12 +609,12 @@ moe_status moe_route(const void* hidden, const void* w_router, const float* rout
     ra.N = P.N;
     ra.d = P.d;
     // batches of up to 32 tokens (bf16, N <= 128): scores and routing in one cluster launch
-    const bool fused = route_fused_supported(P.dtype, P.B, P.N, P.kslots);
-    cudaError_t e = fused ? cudaSuccess : launch_router(ra, P.dtype, s);
+    const bool fused = !scores && route_fused_supported(P.dtype, P.B, P.N, P.kslots);
+    cudaError_t e = fused || scores ? cudaSuccess : launch_router(ra, P.dtype, s);
     if (e != cudaSuccess) return cuda_fail(e, "router launch");
 
     RouteArgs a{};
-    a.logits = ra.logits;
+    a.logits = scores ? scores : ra.logits;
     a.B = P.B;
     a.B_valid = P.B_valid;
     a.N = P.N;
@@ -644,10 +653,77 @@ moe_status moe_route(const void* hidden, const void* w_router, const float* rout
         a.uwords = hdr->union_words;
         a.epoch = next_epoch();
     }
-    e = fused ? launch_route_fused(ra, a, s) : launch_route(a, s);
+    const SelectArgs* sel = select ? &sa : nullptr;
+    e = fused ? launch_route_fused(ra, a, sel, s) : launch_route(a, sel, s);
     if (e != cudaSuccess) return cuda_fail(e, "route launch");
     routed(workspace, a.epoch);   // an expert call on this workspace now waits for it
     return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_num_slots(const moe_route_params* params) {
+    Params P;
+    if (resolve(params, P) != MOE_OK) return -1;
+    return P.kslots;
+}
+
+int32_t moe_layer_launches(const moe_route_params* params, int32_t d_ff) {
+    Params P;
+    if (resolve(params, P) != MOE_OK) return -1;
+    if (d_ff <= 0 || d_ff % 64 != 0 || d_ff > 16384) return -1;
+    int32_t n = route_fused_supported(P.dtype, P.B, P.N, P.kslots) ? 1 : (P.B > 0 ? 2 : 1);
+    if (P.B > 0) n += P.dtype == MOE_DTYPE_F32 ? 3 : 1;
+    return n;
+}
+
+size_t moe_workspace_bytes(const moe_route_params* params, int32_t d_ff) {
+    Params P;
+    if (resolve(params, P) != MOE_OK) return 0;
+    if (d_ff < 0 || d_ff % 64 != 0 || d_ff > 16384) return 0;
+    const WsLayout L = layout(P, d_ff);
+    return d_ff == 0 ? L.hbuf : L.total;
+}
+
+moe_status moe_route(const void* hidden, const void* w_router, const float* router_bias,
+                     const moe_route_params* params, const moe_routing* routing, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream) {
+    return route_impl(hidden, w_router, router_bias, nullptr, nullptr, params, nullptr, routing, workspace,
+                      workspace_bytes, stream);
+}
+
+moe_status moe_route_scores(const float* scores, const float* select_bias, const moe_route_params* params,
+                            const moe_select_params* select, const moe_routing* routing, void* workspace,
+                            size_t workspace_bytes, moe_stream_t stream) {
+    if (!select) return fail(MOE_ERR_ARG, "select is NULL");
+    if (!params) return fail(MOE_ERR_ARG, "params is NULL");
+    if (!scores && params->B != 0) return fail(MOE_ERR_ARG, "scores is NULL");
+    static const float none = 0.f;   // an empty batch reads no score
+    return route_impl(nullptr, nullptr, nullptr, scores ? scores : &none, select_bias, params, select, routing,
+                      workspace, workspace_bytes, stream);
+}
+
+moe_status moe_route_grouped(const void* hidden, const void* w_router, const float* router_bias,
+                             const float* select_bias, const moe_route_params* params,
+                             const moe_select_params* select, const moe_routing* routing, void* workspace,
+                             size_t workspace_bytes, moe_stream_t stream) {
+    if (!select) return fail(MOE_ERR_ARG, "select is NULL");
+    return route_impl(hidden, w_router, router_bias, nullptr, select_bias, params, select, routing, workspace,
+                      workspace_bytes, stream);
+}
+
+moe_status moe_decode_layer_grouped(const void* hidden, const void* w_router, const float* router_bias,
+                                    const float* select_bias, const void* w_gate, const void* w_up,
+                                    const void* w_down, int32_t d_ff, const moe_route_params* params,
+                                    const moe_select_params* select, const moe_routing* routing, void* out,
+                                    void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    const moe_status st = moe_route_grouped(hidden, w_router, router_bias, select_bias, params, select, routing,
+                                            workspace, workspace_bytes, stream);
+    if (st != MOE_OK) return st;
+    return moe_expert_ffn(hidden, w_gate, w_up, w_down, d_ff, params, routing, out, workspace, workspace_bytes,
+                          stream);
 }
 
 moe_status moe_expert_ffn(const void* hidden, const void* w_gate, const void* w_up, const void* w_down,

@@ -119,23 +119,123 @@ struct RouteSmem {
 };
 
 // Writes the routing of token i (this CTA's token il): lane r < cnt holds
-// slot r (myid, myval).
-__device__ __forceinline__ void finish_token(const RouteArgs& a, RouteSmem& sm, int i, int il, int lane, int cnt,
-                                             int myid, float myval) {
-    const float l0 = __shfl_sync(kFull, myval, 0);
-    const float ex = lane < cnt ? expf(myval - l0) : 0.f;
-    const float z = warp_sum(ex);
+// slot r (expert myid, weight w).
+__device__ __forceinline__ void store_token(const RouteArgs& a, RouteSmem& sm, int i, int il, int lane, int cnt,
+                                            int myid, float w) {
     if (lane == 0) a.nused[i] = cnt;
     for (int r = lane; r < a.rbd; r += 32) a.ycnt[(size_t)i * a.rbd + r] = (uint32_t)cnt;
     if (lane < a.kslots) {
         const size_t q = (size_t)i * a.kslots + lane;
         const bool used = lane < cnt;
         a.idx[q] = used ? myid : -1;
-        a.w[q] = used ? ex / z : 0.f;
+        a.w[q] = used ? w : 0.f;
         sm.sidx[il * a.kslots + lane] = used ? myid : -1;
         if (used) atomicOr(&sm.bits[myid], 1u << il);
         else a.pos_of[q] = -1;
     }
+}
+
+// store_token with the softmax over the kept scores as the weights: lane
+// r < cnt holds slot r's score.
+__device__ __forceinline__ void finish_token(const RouteArgs& a, RouteSmem& sm, int i, int il, int lane, int cnt,
+                                             int myid, float myval) {
+    const float l0 = __shfl_sync(kFull, myval, 0);
+    const float ex = lane < cnt ? expf(myval - l0) : 0.f;
+    const float z = warp_sum(ex);
+    store_token(a, sm, i, il, lane, cnt, myid, ex / z);
+}
+
+// Selection by softmax or sigmoid scores with a bias and expert groups
+// (moe_select_params), for one token by one warp; lane l holds experts l,
+// l + 32, ...  `row` is the token's scores.
+template <int NPL>
+__device__ __forceinline__ void select_token(const RouteArgs& a, const SelectArgs& sel, RouteSmem& sm, const float* row,
+                                             int i, int il, int lane, bool& nonfinite) {
+    const int N = a.N;
+    float x[NPL], top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const int e = lane + 32 * j;
+        x[j] = e < N ? row[e] : -INFINITY;
+        if (e < N && !isfinite(x[j])) { nonfinite = true; x[j] = -INFINITY; }
+        top = fmaxf(top, x[j]);
+    }
+    // p: the score, in the softmax's case without its common divisor Z yet
+    float Z = 1.f;
+    if (!sel.sigmoid) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        float zl = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j)
+            if (x[j] != -INFINITY) zl += expf(x[j] - top);
+        Z = warp_sum(zl);
+    }
+    auto score = [&](float v) { return sel.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / Z; };
+    const bool by_x = !sel.sigmoid && !sel.bias && sel.group_top == 1;   // the softmax keeps the order
+    uint32_t kv[NPL];
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        kv[j] = 0;
+        if (x[j] == -INFINITY) continue;
+        float v = x[j];
+        if (!by_x) {
+            v = score(v);
+            if (sel.bias) v += sel.bias[lane + 32 * j];
+        }
+        if (isfinite(v)) kv[j] = score_key(v); else nonfinite = true;
+    }
+    if (sel.n_group > 1) {
+        // lane g holds group g's value
+        const int gs = N / sel.n_group;
+        uint32_t gkey = 0;
+        for (int g = 0; g < sel.n_group; ++g) {
+            uint32_t k1 = 0, k2 = 0;   // the lane's two largest of the group
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                const int e = lane + 32 * j;
+                const uint32_t k = e >= g * gs && e < (g + 1) * gs ? kv[j] : 0u;
+                if (k > k1) { k2 = k1; k1 = k; } else if (k > k2) k2 = k;
+            }
+            const uint32_t m1 = __reduce_max_sync(kFull, k1);
+            float v = m1 ? key_score(m1) : 0.f;
+            if (sel.group_top == 2) {
+                const int owner = __ffs(__ballot_sync(kFull, k1 == m1)) - 1;
+                const uint32_t m2 = __reduce_max_sync(kFull, lane == owner ? k2 : k1);
+                if (m2) v += key_score(m2);
+            }
+            if (lane == g && m1) gkey = score_key(v);
+        }
+        uint32_t stay = 0;
+        for (int r = 0; r < sel.topk_group; ++r) {
+            const uint32_t mine = (stay >> lane) & 1u ? 0u : gkey;
+            const uint32_t m = __reduce_max_sync(kFull, mine);
+            if (m == 0) break;
+            stay |= 1u << (__ffs(__ballot_sync(kFull, mine == m)) - 1);
+        }
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const int e = lane + 32 * j;
+            if (e < N && !((stay >> (e / gs)) & 1u)) kv[j] = 0;
+        }
+    }
+    uint32_t taken = 0;
+    int myid = -1, n = 0;
+    for (int r = 0; r < a.k; ++r) {
+        int id;
+        const uint32_t m = warp_best<NPL>(kv, taken, lane, id);
+        if (m == 0) break;
+        if ((id & 31) == lane) taken |= 1u << (id >> 5);
+        if (lane == r) myid = id;
+        n = r + 1;
+    }
+    float w = lane < n ? score(row[myid]) : 0.f;
+    if (sel.renorm) {
+        const float z = warp_sum(w);
+        w = z > 0.f ? w / z : 0.f;
+    }
+    if (lane == 0 && a.n_base) a.n_base[i] = n;
+    store_token(a, sm, i, il, lane, n, myid, w * sel.scale);
 }
 
 // Publishes the OEA union S_base: lane j stores word j (bit b: expert
@@ -175,8 +275,9 @@ __device__ __forceinline__ void route_prepare(const RouteArgs& a, unsigned char*
 // cluster, from the scores at `logits` (global or shared memory).  Prepared:
 // the caller has run route_prepare and synchronised the CTA after its
 // dependency wait.
-template <int NPL, bool kPrepared>
-__device__ __forceinline__ void route_body(const RouteArgs& a, const float* logits, unsigned char* smem_raw,
+// kSelect: moe_select_params instead of plain top-k or OEA.
+template <int NPL, bool kPrepared, bool kSelect>
+__device__ __forceinline__ void route_body(const RouteArgs& a, const SelectArgs& sel, const float* logits, unsigned char* smem_raw,
                                            const uint32_t rank, const uint32_t ncta) {
     const int nthreads = blockDim.x;
     const int nwarps = nthreads >> 5;
@@ -205,7 +306,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const float* logi
     }
 
     bool nonfinite = false;
-    const bool oea = a.mode == MOE_MODE_OEA;
+    const bool oea = !kSelect && a.mode == MOE_MODE_OEA;
     const bool keep_keys = te - tb <= nwarps;   // one token per warp: keys and picks stay in registers
     uint32_t kv[NPL];
     // Phase-1 picks of this warp's token (used by phase 2 when keep_keys).
@@ -216,8 +317,12 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const float* logi
     // ---- plain top-k, or OEA phase 1 (baseline and union) ------------------
     for (int i = tb + warp; i < te; i += nwarps) {
         const int il = i - tb;
+        if (kSelect && i < a.B_valid) {
+            select_token<NPL>(a, sel, sm, logits + (size_t)i * N, i, il, lane, nonfinite);
+            continue;
+        }
         load_keys<NPL>(logits + (size_t)i * N, N, lane, kv, nonfinite);
-        if (i >= a.B_valid) {           // padding token: selects nothing
+        if (kSelect || i >= a.B_valid) {   // padding token: selects nothing
             if (lane == 0) {
                 sm.snb[il] = 0;
                 if (a.n_base && !oea) a.n_base[i] = 0;   // OEA: after S_base is published
@@ -456,10 +561,10 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const float* logi
     if (ncta > 1) cluster_sync();   // no CTA leaves while another may still read its words
 }
 
-template <int NPL>
-__global__ void route_kernel(RouteArgs a) {
+template <int NPL, bool kSelect>
+__global__ void route_kernel(RouteArgs a, SelectArgs sel) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    route_body<NPL, false>(a, a.logits, smem_raw, cluster_ctarank(), gridDim.x);   // the whole grid is one cluster
+    route_body<NPL, false, kSelect>(a, sel, a.logits, smem_raw, cluster_ctarank(), gridDim.x);   // the whole grid is one cluster
 }
 
 // ---- scores and routing in one cluster (bf16, up to 32 tokens, N <= 128) ----
@@ -504,8 +609,8 @@ __host__ __device__ constexpr size_t fused_smem_bytes(int N, int kslots) {
            (size_t)kFusedWarps * 512 * 4;
 }
 
-template <int NPL>
-__global__ void __launch_bounds__(kFusedWarps * 32, 1) route_fused_kernel(RouterArgs r, RouteArgs a) {
+template <int NPL, bool kSelect>
+__global__ void __launch_bounds__(kFusedWarps * 32, 1) route_fused_kernel(RouterArgs r, RouteArgs a, SelectArgs sel) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const size_t rsm = (route_smem_bytes(a.N, a.kslots) + 15) & ~size_t(15);
     float* lg = reinterpret_cast<float*>(smem_raw + rsm);             // [32][N] scores (CTA 0)
@@ -587,11 +692,11 @@ __global__ void __launch_bounds__(kFusedWarps * 32, 1) route_fused_kernel(Router
     if (rank != 0) return;
     // the routing reads every argument from the kernel's parameters and the
     // scores from shared memory
-    route_body<NPL, true>(a, lg, smem_raw, 0u, 1u);
+    route_body<NPL, true, kSelect>(a, sel, lg, smem_raw, 0u, 1u);
 }
 
-template <int NPL>
-cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, cudaStream_t s) {
+template <int NPL, bool kSelect>
+cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int ncta = (a.N + 15) / 16;
     const size_t smem = fused_smem_bytes(a.N, a.kslots);
     static bool attr_set[64] = {};
@@ -600,7 +705,7 @@ cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, cudaSt
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(route_fused_kernel<NPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
+        e = cudaFuncSetAttribute(route_fused_kernel<NPL, kSelect>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
@@ -618,11 +723,11 @@ cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, cudaSt
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ncta > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, route_fused_kernel<NPL>, r, a);
+    return cudaLaunchKernelEx(&cfg, route_fused_kernel<NPL, kSelect>, r, a, sel);
 }
 
-template <int NPL>
-cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
+template <int NPL, bool kSelect>
+cudaError_t launch_route_t(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int threads = NPL <= 8 ? 1024 : 512;
     const int ncta = a.B > 0 ? (a.B + 31) / 32 : 1;
     const size_t smem = 4 * 32 * 4 + 3 * (size_t)a.N * 4 + 32 * (size_t)a.kslots * 4;
@@ -641,7 +746,7 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ncta > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, route_kernel<NPL>, a);
+    return cudaLaunchKernelEx(&cfg, route_kernel<NPL, kSelect>, a, sel);
 }
 
 }  // namespace
@@ -650,21 +755,35 @@ bool route_fused_supported(int dtype, int B, int N, int kslots) {
     return dtype == MOE_DTYPE_BF16 && B > 0 && B <= 32 && N <= 128 && fused_smem_bytes(N, kslots) <= smem_cap();
 }
 
-cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, cudaStream_t s) {
+namespace {
+
+template <bool kSelect>
+cudaError_t launch_route_fused_s(const RouterArgs& r, const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int nw = (a.N + 31) / 32;
-    if (nw <= 1) return launch_route_fused_t<1>(r, a, s);
-    if (nw <= 2) return launch_route_fused_t<2>(r, a, s);
-    return launch_route_fused_t<4>(r, a, s);
+    if (nw <= 1) return launch_route_fused_t<1, kSelect>(r, a, sel, s);
+    if (nw <= 2) return launch_route_fused_t<2, kSelect>(r, a, sel, s);
+    return launch_route_fused_t<4, kSelect>(r, a, sel, s);
 }
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+template <bool kSelect>
+cudaError_t launch_route_s(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int nw = (a.N + 31) / 32;
-    if (nw <= 1) return launch_route_t<1>(a, s);
-    if (nw <= 2) return launch_route_t<2>(a, s);
-    if (nw <= 4) return launch_route_t<4>(a, s);
-    if (nw <= 8) return launch_route_t<8>(a, s);
-    if (nw <= 16) return launch_route_t<16>(a, s);
-    return launch_route_t<32>(a, s);
+    if (nw <= 1) return launch_route_t<1, kSelect>(a, sel, s);
+    if (nw <= 2) return launch_route_t<2, kSelect>(a, sel, s);
+    if (nw <= 4) return launch_route_t<4, kSelect>(a, sel, s);
+    if (nw <= 8) return launch_route_t<8, kSelect>(a, sel, s);
+    if (nw <= 16) return launch_route_t<16, kSelect>(a, sel, s);
+    return launch_route_t<32, kSelect>(a, sel, s);
+}
+
+}  // namespace
+
+cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
+    return sel ? launch_route_fused_s<true>(r, a, *sel, s) : launch_route_fused_s<false>(r, a, SelectArgs{}, s);
+}
+
+cudaError_t launch_route(const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
+    return sel ? launch_route_s<true>(a, *sel, s) : launch_route_s<false>(a, SelectArgs{}, s);
 }
 
 }  // namespace moe

@@ -400,6 +400,226 @@ moe_status moe_decode_layer(const void *hidden, const void *w_router, const floa
                             size_t workspace_bytes, moe_stream_t stream);
 
 /*
+ * Routing for models whose router is not a plain top-k of the scores: the
+ * experts are scored by a softmax or a sigmoid, a per-expert bias (learnt to
+ * balance the experts' load) shifts the selection but not the weights, and
+ * the selection may be limited to the best few of n_group equal groups of
+ * consecutive experts.  For a token with router scores x[N]:
+ *   p_e   = softmax(x)_e or 1 / (1 + exp(-x_e));
+ *   v_e   = p_e + bias_e, the selection value;
+ *   group value: the sum of the group's group_top (1 or 2) largest v; the
+ *           topk_group groups of largest value stay, equal values by the
+ *           lower group;
+ *   the k largest v_e of the groups that stay are chosen, in that order,
+ *           equal values by the lower expert id;
+ *   w_e   = p_e, over the sum of the chosen p if renormalise (0 where that
+ *           sum is 0), times scale.
+ * A softmax without a bias and with group_top 1 is ranked by x itself,
+ * which it keeps in order.  An expert whose x or v is not finite is never
+ * chosen (a token may then keep fewer than k experts) and raises
+ * MOE_FLAG_NONFINITE_SCORE.  All arithmetic is fp32.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+#define MOE_MAX_GROUPS 32
+
+typedef struct {
+    int32_t score;       /* moe_score                                             */
+    int32_t n_group;     /* groups, 1..MOE_MAX_GROUPS, a divisor of N             */
+    int32_t topk_group;  /* groups that stay, 1..n_group                          */
+    int32_t group_top;   /* 1 or 2 (at most N / n_group): values in a group's sum */
+    int32_t renormalise; /* 0 or 1                                                */
+    float scale;         /* factor of the weights, finite                         */
+} moe_select_params;
+
+/*
+ * Selection and grouping (as above) of the caller's router scores.
+ *   scores      [B][N] fp32.
+ *   select_bias [N] fp32, nullable.
+ *   params      mode must be MOE_MODE_TOPK; k at most the experts of the
+ *               groups that stay.
+ *   routing     as for moe_route (logits is not written).
+ * Afterwards moe_expert_ffn or moe_expert_ffn_mixed may follow on the same
+ * workspace, as after moe_route.
+ */
+moe_status moe_route_scores(const float *scores, const float *select_bias, const moe_route_params *params,
+                            const moe_select_params *select, const moe_routing *routing, void *workspace,
+                            size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_route with this selection: router scores (router_bias added to the
+ * scores, select_bias to the selection values), selection and grouping.
+ */
+moe_status moe_route_grouped(const void *hidden, const void *w_router, const float *router_bias,
+                             const float *select_bias, const moe_route_params *params,
+                             const moe_select_params *select, const moe_routing *routing, void *workspace,
+                             size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_route_grouped followed by moe_expert_ffn on the same stream. */
+moe_status moe_decode_layer_grouped(const void *hidden, const void *w_router, const float *router_bias,
+                                    const float *select_bias, const void *w_gate, const void *w_up,
+                                    const void *w_down, int32_t d_ff, const moe_route_params *params,
+                                    const moe_select_params *select, const moe_routing *routing, void *out,
+                                    void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The attention half of a decoder block, for tokens that are decoded or
+ * drafted: keys and values live in pages, moe_kv_append rotates a step's
+ * queries and keys and writes its keys and values into their pages, and
+ * moe_tree_attention attends from the step's tokens to the cache.  No page
+ * of the method describes them; they are the library's own addition.
+ *
+ * A cache holds, for every page, key head and row of the page, one vector
+ * of head_dim components:
+ *   k, v        [n_pages][kv_heads][page_size][head_dim] dtype, device,
+ *               16-byte aligned.
+ *   page_table  [n_requests][max_pages] int32, device: entry j of a request
+ *               is the page of its positions j * page_size and on.  Read by
+ *               moe_tree_attention only (NULL is allowed for moe_kv_append).
+ *   head_dim    a multiple of 8, 8..256.  page_size: 1..65536.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    const int32_t *page_table;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t n_requests;
+    int32_t max_pages;
+    int32_t dtype;
+} moe_kv_cache;
+
+#define MOE_MAX_HEAD_DIM 256
+#define MOE_MAX_PAGE 65536
+#define MOE_MAX_REQUESTS 1024
+
+/*
+ * Rotation angles: position m turns pair i (0 <= i < rot / 2) by m * f_i,
+ * f_i = base^(-2 i / rot), or scaled for contexts longer than a model was
+ * trained on:
+ *   MOE_ROPE_LINEAR  f_i / factor (positions are interpolated);
+ *   MOE_ROPE_NTK     base * factor^(rot / (rot - 2)) in place of base;
+ *   MOE_ROPE_YARN    (Peng et al., "YaRN", 2023) pairs that turn more than
+ *                    beta_fast times over original_len positions keep f_i,
+ *                    pairs that turn less than beta_slow times take
+ *                    f_i / factor, with a linear ramp over the pair index
+ *                    between the two (its ends rounded outwards to whole
+ *                    indices); cosines and sines are multiplied by
+ *                    0.1 ln(factor) + 1, unless `magnitude` is positive.
+ *   magnitude        factor of every cosine and sine; <= 0: 1 (YaRN: the
+ *                    value above).
+ */
+typedef enum { MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3 } moe_rope_scaling;
+
+typedef struct {
+    int32_t rot;         /* rotated components, even, 2..MOE_MAX_HEAD_DIM (NTK: 4..) */
+    int32_t scaling;     /* moe_rope_scaling                                         */
+    double base;         /* > 1                                                      */
+    double factor;       /* >= 1 (not read by MOE_ROPE_PLAIN)                        */
+    double original_len; /* YaRN: > 0                                                */
+    double beta_fast;    /* YaRN: > beta_slow                                        */
+    double beta_slow;    /* YaRN: > 0                                                */
+    double magnitude;
+} moe_rope_params;
+
+/*
+ * Writes the table that moe_kv_append reads: table[n_pos][rot] fp32, row m
+ * the rot/2 cosines of position m's angles, then their sines (angles and
+ * functions in fp64, rounded once).  Made once per model.
+ */
+moe_status moe_rope_table(const moe_rope_params *params, int32_t n_pos, float *table, moe_stream_t stream);
+
+/*
+ * Rotates the queries and keys of T tokens and writes keys and values into
+ * the cache.
+ *   q [T][heads][head_dim], k and v [T][kv_heads][head_dim], dtype of the
+ *             cache: components of a head are adjacent; *_tok and *_head
+ *             are the distances, in elements, between tokens and between
+ *             heads (slices of one projection's output serve as they are),
+ *             each a multiple of 16 bytes.  16-byte aligned.
+ *             q and q_out may both be NULL (keys and values only).
+ *   rope      [n_pos][rot] fp32 (moe_rope_table); components rot.. of a
+ *             head are not rotated.  rot 0: no rotation, rope NULL.
+ *   interleaved  0: pair i is (i, i + rot/2); 1: (2i, 2i + 1).
+ *   positions [T] int32: rows of rope.  One outside 0..n_pos-1 raises
+ *             MOE_FLAG_BAD_INDEX and the nearest row is taken.  Not read
+ *             with rot 0.
+ *   slots     [T] int64: page * page_size + row of the page.  A negative
+ *             slot writes no key and value (padding); one past the cache
+ *             raises MOE_FLAG_BAD_INDEX and writes none.  Two tokens of a
+ *             call must not share a slot.
+ *   q_out     rotated queries; may be q itself with the same distances.
+ * A pair (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, rounded
+ * once.  The workspace holds the flag word: MOE_ATTENTION_WORKSPACE_MIN
+ * bytes (or more), zero-filled once before its first use.
+ */
+typedef struct {
+    int32_t T;
+    int32_t heads;
+    int32_t rot;
+    int32_t n_pos;
+    int32_t interleaved;
+    int64_t q_tok, q_head;
+    int64_t k_tok, k_head;
+    int64_t v_tok, v_head;
+    int64_t out_tok, out_head;
+} moe_append_params;
+
+#define MOE_ATTENTION_WORKSPACE_MIN 512
+
+moe_status moe_kv_append(const void *q, const void *k, const void *v, const float *rope, const int32_t *positions,
+                         const int64_t *slots, const moe_append_params *params, const moe_kv_cache *cache,
+                         void *q_out, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * Attention of the step's tokens to their requests' caches.
+ *   q          [T][heads][head_dim], cache's dtype, distances as above.
+ *              Query head h reads key head h / (heads / kv_heads).
+ *   q_offsets  [n_requests + 1] int32, device: tokens q_offsets[r] ..
+ *              q_offsets[r + 1] - 1 are request r's, in the order in which
+ *              they sit in its cache.  Ascending from 0, the last at most T.
+ *   ctx_len    [n_requests] int32, device: positions before the step.  The
+ *              request's token i is at position ctx_len + i, written before
+ *              the call (moe_kv_append).
+ *   mask       [T][mask_words] uint32, device, nullable: token t sees every
+ *              position before ctx_len, and its request's token j if bit
+ *              j % 32 of word j / 32 of its row is set (a draft tree: its
+ *              ancestors and itself); tokens past 32 * mask_words are not
+ *              seen.  NULL: token i sees tokens 0..i.
+ *   out        [T][heads][head_dim], dense: sum_j softmax(scale q.k)_j v_j.
+ *   lse        [T][heads] fp32, nullable: ln sum_j exp(scale q.k_j).
+ * A token that sees nothing gets zeros and an lse of -inf.  Tokens past
+ * q_offsets[n_requests] are not written.  What lies in positions that no
+ * token of the request sees, and in rows of its pages past its length, has
+ * no influence whatever its value.
+ * A request whose length does not fit max_pages, whose page is outside
+ * 0..n_pages-1, or whose q_offsets or ctx_len are out of range raises
+ * MOE_FLAG_BAD_INDEX; its output is unspecified, other requests are not
+ * affected.
+ * Products and sums are fp32; bf16: the exponentials are rounded to bf16
+ * before the product with V (tensor cores), their sum is not.
+ * n_requests at most MOE_MAX_REQUESTS.
+ */
+typedef struct {
+    int32_t T;
+    int32_t heads;
+    int32_t mask_words;
+    float scale;
+    int64_t q_tok, q_head;
+} moe_attention_params;
+
+/* Workspace for up to T tokens of `heads` query heads on this cache (its
+ * buffers are not read); 0 if the arguments are invalid.  256-byte aligned,
+ * zero-filled once before its first use.  It serves moe_kv_append too. */
+size_t moe_attention_workspace_bytes(int32_t T, int32_t heads, const moe_kv_cache *cache);
+
+moe_status moe_tree_attention(const void *q, const int32_t *q_offsets, const int32_t *ctx_len, const uint32_t *mask,
+                              const moe_attention_params *params, const moe_kv_cache *cache, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
  * moe_decode_layer for callers that cannot allocate device memory.  The
  * pages have no counterpart: this is a property of the library, not of the
  * method.  A plugin whose host engine owns all device memory, a runtime
