@@ -388,6 +388,18 @@ moe_status tc_operand_maps(unsigned char* ws, const WsLayout& L, const void* hid
     return MOE_OK;
 }
 
+}  // namespace
+
+namespace {
+// Bound of every in-kernel wait (moe_set_wait_timeout_us), microseconds.
+constexpr uint32_t kDefaultWaitUs = 2000000u;
+std::atomic<uint32_t> g_wait_us{kDefaultWaitUs};
+}  // namespace
+
+namespace moe {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode(); }
+
+// SMs of the current device; 0: unknown.
 int num_sms() {
     static int cache[64] = {0};
     int dev = 0;
@@ -400,15 +412,6 @@ int num_sms() {
     return cache[dev];
 }
 
-}  // namespace
-
-namespace {
-// Bound of every in-kernel wait (moe_set_wait_timeout_us), microseconds.
-constexpr uint32_t kDefaultWaitUs = 2000000u;
-std::atomic<uint32_t> g_wait_us{kDefaultWaitUs};
-}  // namespace
-
-namespace moe {
 // SM cycles per microsecond assumed for the wait bound: the GB300's SM
 // clock is at most 2.07 GHz, so a bound of t microseconds lasts at least
 // about t microseconds.

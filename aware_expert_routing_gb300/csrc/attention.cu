@@ -9,6 +9,8 @@
 
 namespace moe {
 
+int num_sms();   // api.cu
+
 namespace {
 
 // One block per (token, query head): its warps take positions in turn, a
@@ -90,6 +92,7 @@ __global__ void __launch_bounds__(kSimpleWarps * 32) attention_simple_kernel(Att
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, int dtype, cudaStream_t s) {
+    if (attention_tc_supported(a, dtype)) return launch_attention_tc(a, num_sms(), s);
     const dim3 grid(a.T, a.heads);
     if (dtype == MOE_DTYPE_BF16) attention_simple_kernel<__nv_bfloat16><<<grid, kSimpleWarps * 32, 0, s>>>(a);
     else attention_simple_kernel<float><<<grid, kSimpleWarps * 32, 0, s>>>(a);
@@ -106,6 +109,7 @@ namespace {
 moe_status check_heads(int T, int heads, const moe_kv_cache* cache) {
     if (T < 0) return report(MOE_ERR_ARG, "T=%d is negative", T);
     if (heads < 1 || heads > kMaxHeads) return report(MOE_ERR_ARG, "heads=%d outside 1..%d", heads, kMaxHeads);
+    if ((long long)T * heads > 0x7fffffffLL) return report(MOE_ERR_ARG, "T * heads passes 2^31 - 1");
     if (heads % cache->kv_heads != 0)
         return report(MOE_ERR_ARG, "heads=%d is not a multiple of kv_heads=%d", heads, cache->kv_heads);
     return MOE_OK;
@@ -116,7 +120,7 @@ extern "C" {
 
 size_t moe_attention_workspace_bytes(int32_t T, int32_t heads, const moe_kv_cache* cache) {
     if (check_cache(cache, true) != MOE_OK || check_heads(T, heads, cache) != MOE_OK) return 0;
-    return MOE_ATTENTION_WORKSPACE_MIN;
+    return attention_layout(T, heads / cache->kv_heads, cache->head_dim).total;
 }
 
 moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int32_t* ctx_len, const uint32_t* mask,
@@ -147,6 +151,14 @@ moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int
     a.n_pages = cache->n_pages; a.page_size = cache->page_size; a.max_pages = cache->max_pages;
     a.mask_words = mask ? p->mask_words : 0;
     a.scale = p->scale; a.q_tok = p->q_tok; a.q_head = p->q_head;
+    const AttentionLayout L = attention_layout(p->T, p->heads / cache->kv_heads, cache->head_dim);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.total = reinterpret_cast<long long*>(ws + L.plan);
+    a.plan = reinterpret_cast<RangeStart*>(ws + L.plan + 16);
+    a.ml = reinterpret_cast<float2*>(ws + L.ml);
+    a.o = reinterpret_cast<float*>(ws + L.o);
+    a.rows = L.rows;
+    a.wait_cycles = wait_cycles_now();
     const cudaError_t e = launch_attention(a, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : report(MOE_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
 }

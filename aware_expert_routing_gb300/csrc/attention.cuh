@@ -48,6 +48,39 @@ inline moe_status check_cache(const moe_kv_cache* c, bool attend) {
     return MOE_OK;
 }
 
+// Work of the tensor-core kernel is cut into this many equal ranges at most
+// (one per SM of a GB300), each range's ends leaving partial sums behind.
+constexpr int kAttentionRanges = 152;
+constexpr int kAttentionRows = 256;   // most query rows of a work unit
+
+// Workspace of moe_tree_attention: the flag word's header, the record of each
+// range's start, and two partial results a range (of its first and its last
+// unit): per row the running maximum (of scores in powers of two) and sum,
+// and the unnormalised output.
+struct AttentionLayout {
+    size_t plan, ml, o, total;
+    int rows;
+};
+
+struct RangeStart {
+    int t0, n;          // the request's tokens
+    int h, rt;          // key head and row tile of the unit that the range starts in
+    int kt, nkt;        // first key tile, and the unit's key tiles
+    int pad[2];
+};
+
+inline AttentionLayout attention_layout(int T, int group, int D) {
+    AttentionLayout L;
+    const long long rows = (long long)T * group;
+    L.rows = (int)(rows < kAttentionRows ? rows : kAttentionRows);
+    size_t o = align256(MOE_ATTENTION_WORKSPACE_MIN);
+    L.plan = o; o += align256(16 + sizeof(RangeStart) * kAttentionRanges);
+    L.ml = o;   o += align256(sizeof(float2) * 2 * kAttentionRanges * (size_t)L.rows);
+    L.o = o;    o += align256(sizeof(float) * 2 * kAttentionRanges * (size_t)L.rows * D);
+    L.total = o;
+    return L;
+}
+
 struct AppendArgs {
     const void *q, *k, *v;
     const float* rope;
@@ -73,7 +106,18 @@ struct AttentionArgs {
     int T, heads, kv_heads, D, R, n_pages, page_size, max_pages, mask_words;
     float scale;
     long long q_tok, q_head;
+    // tensor-core kernel: its part of the workspace (AttentionLayout)
+    long long* total;          // work of all requests, in key tiles
+    RangeStart* plan;          // [kAttentionRanges]
+    float2* ml;                // [2 * ranges][rows]
+    float* o;                  // [2 * ranges][rows][D]
+    int rows;
+    long long wait_cycles;
 };
+
+// Tensor-core kernel (attention_tc.cu).
+bool attention_tc_supported(const AttentionArgs& a, int dtype);
+cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t s);
 
 #ifdef __CUDACC__
 

@@ -1,0 +1,837 @@
+// attention_tc.cu -- moe_tree_attention on the 5th-generation tensor cores:
+// bf16 caches with heads of 64 or 128 components and pages that tile evenly.
+//
+// For the query rows of one key head (every drafted token of a request times
+// the query heads that share the key head, up to 128 rows a tile), over tiles
+// of 128 keys:
+//   S = Q K^T;  m' = max(m, rowmax S);  P = exp(scale (S - m'));
+//   l = l exp(scale (m - m')) + rowsum P;  O = O exp(scale (m - m')) + P V;
+// and at the end O / l.  Keys and values are read once per unit of work, so
+// the cache's bytes bound the kernel while a key head has fewer than about
+// 250 rows.
+//
+//   * Work.  A unit is (request, key head, tile of rows); its key tiles follow
+//     one another in one line with those of all other units, and each CTA (one
+//     per SM) takes an equal stretch of the line, whatever the requests'
+//     lengths.  A unit that lies in one stretch is finished there; one that is
+//     cut leaves partial (m, l, O) per stretch, which the joining kernel below
+//     adds up in the order of the stretches, so results repeat bit for bit.
+//     Lengths are read on the device: nothing depends on the host knowing them.
+//   * A producer warp copies pages with TMA into a ring of key and value tiles
+//     (8-row swizzle atoms side by side, so that pages of any number of atoms
+//     make one operand), one thread issues the MMAs, and one warpgroup per row
+//     tile does the softmax from tensor memory, a row a thread.
+//   * S sits in two buffers of tensor memory.  With one row tile a unit (up to
+//     128 rows) the next tile's S is computed while the softmax works on this
+//     one; with two (up to 256 rows) each has a buffer and they take turns, and
+//     each tile of keys and values is read once for both.
+//   * P replaces S in tensor memory (bf16) and is the A operand of P V.
+//   * O is corrected only when a row's maximum has grown by more than 8 powers
+//     of two since the last correction (P then stays below 2^8, exact in the
+//     sums), so almost never after the first tiles.
+//   * Drafted positions: a row's mask words become 128 bits per key tile; only
+//     tiles that reach past the context look at them.  Value rows past the
+//     length are zeroed before the product (0 times whatever lies there must be
+//     0), and so are drafted rows that are not finite: rows that see one become
+//     NaN through l, the others are not touched.
+#include <cudaTypedefs.h>
+
+#include "attention.cuh"
+
+namespace moe {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // api.cu
+
+namespace {
+
+constexpr int kKeys = 128;     // keys per tile
+constexpr int kRowsTile = 128; // query rows per tile
+constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O from here
+constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
+
+// Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
+// (taddr >> 16) + l, from column taddr & 0xffff; complete on return.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
+        "}, [%128];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+        "}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Whole warp: the converse store (tmem_wait_st() completes it).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
+        "};"
+        ::"r"(taddr),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Descriptor of an MN-major operand in 128-byte swizzle atoms of 8 K-rows by
+// 64 elements: atoms `lbo` bytes apart along MN and `sbo` along K.
+__device__ __forceinline__ uint64_t umma_sdesc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int D, int kTiles>
+struct Cfg {
+    static constexpr int kThreads = 64 + 128 * kTiles;
+    static constexpr int kBlocks = D / 64;              // 64-component blocks of a head
+    static constexpr int kStage = kKeys * D * 2;        // a tile of keys or of values
+    static constexpr int kQTile = kRowsTile * D * 2;
+    static constexpr int kControl = 2048;
+    static constexpr int kSmem = 227 * 1024;
+    static constexpr int kStages = (kSmem - 1024 - kControl - kTiles * kQTile) / kStage;
+    static constexpr int kRows = kRowsTile * kTiles;    // rows of a unit
+};
+
+struct Control {
+    uint64_t full[16], empty[16], q_full[2], s_full[2], p_full[2], pv_done[2];
+    long long scan[16];
+    long long begin, end, total;
+    long long wait_cycles;
+    int start_r, abort_flag;
+    long long start_off;       // key tiles of the start request before this CTA's range
+    uint32_t tmem_base;
+    uint32_t bad[2][2][4];     // per row tile and key tile's parity: keys whose value is not finite
+};
+static_assert(sizeof(Control) <= 2048, "control block");
+
+__device__ __forceinline__ bool aborted(Control& S) { return *(volatile int*)&S.abort_flag != 0; }
+
+// Bounded mbarrier wait; once the CTA has given up every later wait returns
+// at once, so the control flow (and every barrier) still completes.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Control& S, uint32_t* flags) {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!aborted(S)) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (clock64() - t0 > S.wait_cycles) {
+            *(volatile int*)&S.abort_flag = 1;
+            raise_flag(flags, kFlagTimeout);
+            return;
+        }
+    }
+}
+
+struct Request {
+    int t0, n, ctx, nrt, nkt;   // n 0: nothing to do
+};
+
+template <int kRows>
+__device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, bool& bad) {
+    Request q;
+    q.t0 = a.q_offsets[r];
+    const int t1 = a.q_offsets[r + 1];
+    q.ctx = a.ctx_len[r];
+    q.n = t1 - q.t0;
+    bad = q.t0 < 0 || t1 > a.T || t1 < q.t0 ||
+          (q.n > 0 && (q.ctx < 0 || (long long)q.ctx + q.n > (long long)a.max_pages * a.page_size));
+    if (bad) q.n = 0;
+    q.nrt = (q.n * (a.heads / a.kv_heads) + kRows - 1) / kRows;
+    q.nkt = q.n > 0 ? (q.ctx + q.n + kKeys - 1) / kKeys : 0;
+    return q;
+}
+
+// A CTA's stretch of the line, one unit (or its part) at a time.
+template <int kRows>
+struct Walk {
+    Request q;
+    int r, h, rt, kt, nk;       // this part: key tiles kt .. kt + nk - 1
+    long long left;             // key tiles after this part
+    bool first;                 // the stretch's first part
+
+    __device__ __forceinline__ void part() {
+        nk = (int)min((long long)(q.nkt - kt), left);
+        left -= nk;
+    }
+    __device__ __forceinline__ void start(const AttentionArgs& a, const Control& S) {
+        bool bad;
+        r = S.start_r;
+        q = load_request<kRows>(a, r, bad);
+        const long long u = S.start_off / q.nkt;
+        kt = (int)(S.start_off - u * q.nkt);
+        h = (int)(u / q.nrt);
+        rt = (int)(u - (long long)h * q.nrt);
+        left = S.end - S.begin;
+        first = true;
+        part();
+    }
+    __device__ __forceinline__ bool next(const AttentionArgs& a) {
+        if (left <= 0) return false;
+        first = false;
+        kt = 0;
+        if (++rt >= q.nrt) {
+            rt = 0;
+            if (++h >= a.kv_heads) {
+                h = 0;
+                bool bad;
+                do q = load_request<kRows>(a, ++r, bad);
+                while (q.n == 0 && r + 1 < a.R);
+                if (q.n == 0) return false;   // not reached: the line ends with a request that has work
+            }
+        }
+        part();
+        return true;
+    }
+    // rows of row tile w of this unit
+    __device__ __forceinline__ int rows(const AttentionArgs& a, int w) const {
+        return max(0, min(kRowsTile, q.n * (a.heads / a.kv_heads) - rt * kRows - w * kRowsTile));
+    }
+};
+
+// Bits d0 .. d0 + 31 of what token i of n sees among the drafted tokens
+// (negative ones are the context).
+__device__ __forceinline__ uint32_t seen_bits(const uint32_t* mrow, int words, int i, int n, int d0) {
+    if (d0 <= -32) return 0xffffffffu;
+    const int lim = mrow ? n : min(n, i + 1);
+    auto word = [&](int w) -> uint32_t {
+        uint32_t m = mrow ? (w < words ? mrow[w] : 0u) : 0xffffffffu;
+        const int k = lim - 32 * w;
+        return k <= 0 ? 0u : k < 32 ? m & ((1u << k) - 1u) : m;
+    };
+    if (d0 < 0) return ((1u << -d0) - 1u) | (word(0) << -d0);
+    const int w = d0 >> 5, sh = d0 & 31;
+    return sh ? __funnelshift_r(word(w), word(w + 1), sh) : word(w);
+}
+
+template <int D, int kTiles>
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
+attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    using C = Cfg<D, kTiles>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* ring = smem;                                 // [kStages][kStage]
+    unsigned char* qs = smem + C::kStages * C::kStage;          // [kTiles][kQTile]
+    Control& S = *reinterpret_cast<Control*>(qs + kTiles * C::kQTile);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.heads / a.kv_heads;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.q_full[i], 4);
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i], 4);
+            mbar_init(&S.pv_done[i], 1);
+        }
+        fence_barrier_init();
+        S.abort_flag = 0;
+        S.wait_cycles = a.wait_cycles;
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 1) tmem_alloc(&S.tmem_base, 512);
+    grid_launch_dependents();   // the joining kernel may take its place; it waits for this grid's end
+    grid_dependency_wait();     // lengths, queries and the cache come from preceding kernels
+
+    // ---- the line: each thread adds up a few consecutive requests -------------
+    {
+        const int per = (a.R + C::kThreads - 1) / C::kThreads;
+        const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
+        long long sum = 0;
+        for (int r = r0; r < r1; ++r) {
+            bool bad;
+            const Request q = load_request<C::kRows>(a, r, bad);
+            if (bad && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
+            sum += (long long)q.nrt * q.nkt * a.kv_heads;
+        }
+        long long inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += t;
+        }
+        if (lane == 31) S.scan[warp] = inc;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            if (w < warp) before += S.scan[w];
+            total += S.scan[w];
+        }
+        const long long ranges = min((long long)gridDim.x, total);
+        const long long b = ranges > 0 ? total * blockIdx.x / ranges : 0, e = ranges > 0 ? total * (blockIdx.x + 1) / ranges : 0;
+        before += inc - sum;
+        if (threadIdx.x == 0) {
+            const bool mine = blockIdx.x < ranges;
+            S.begin = mine ? b : 0;
+            S.end = mine ? e : 0;
+            if (blockIdx.x == 0) *a.total = total;
+        }
+        if (blockIdx.x < ranges && b >= before && b < before + sum) {
+            long long at = before;
+            for (int r = r0; r < r1; ++r) {
+                bool bad;
+                const Request q = load_request<C::kRows>(a, r, bad);
+                const long long w = (long long)q.nrt * q.nkt * a.kv_heads;
+                if (b < at + w) {
+                    S.start_r = r;
+                    S.start_off = b - at;
+                    break;
+                }
+                at += w;
+            }
+        }
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = S.tmem_base;
+    const bool any = S.end > S.begin;
+    Walk<C::kRows> W;
+    if (any) W.start(a, S);
+    if (any && threadIdx.x == 0) {
+        RangeStart rec;
+        rec.t0 = W.q.t0; rec.n = W.q.n; rec.h = W.h; rec.rt = W.rt; rec.kt = W.kt; rec.nkt = W.q.nkt;
+        rec.pad[0] = rec.pad[1] = 0;
+        a.plan[blockIdx.x] = rec;
+    }
+
+    if (!any) {
+        // no work for this CTA
+    } else if (warp == 0) {
+        // ---- producer: pages into the ring, in the order in which the MMAs read them ----
+        uint32_t seq = 0;
+        const int page = a.page_size;
+        const int per = page < kKeys ? kKeys / page : 1;        // pages of a tile
+        const int prow = page < kKeys ? page : kKeys;           // rows of a copy
+        const uint32_t bytes = (uint32_t)prow * D * 2;
+        do {
+            const int len = W.q.ctx + W.q.n;
+            const int32_t* table = a.page_table + (size_t)W.r * a.max_pages;
+            // lane i: first 8-row group of copy i of tile j (or -1)
+            auto group_of = [&](int j) -> int {
+                const int pos = (W.kt + j) * kKeys + lane * prow;
+                if (j >= W.nk || lane >= per || pos >= len) return -1;
+                int id = table[pos / page];
+                if (id < 0 || id >= a.n_pages) {
+                    raise_flag(a.flags, kFlagBadIndex);
+                    id = 0;
+                }
+                return (int)((((long long)id * a.kv_heads + W.h) * page + pos % page) / 8);
+            };
+            auto load = [&](const CUtensorMap* map, int g) {
+                const uint32_t st = seq % C::kStages, ph = (seq / C::kStages) & 1;
+                wait_bar(&S.empty[st], ph ^ 1, S, a.flags);
+                ++seq;
+                const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
+                if (aborted(S)) return;
+                if (lane == 0) mbar_arrive_expect_tx(&S.full[st], n * bytes);
+                __syncwarp();
+                if (g >= 0) tma_load_4d(smem_u32(ring + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &S.full[st]);
+            };
+            int g_prev = -1, g = group_of(0);
+            for (int j = 0; j < W.nk; ++j) {
+                const int g_next = group_of(j + 1);
+                load(&map_k, g);
+                if (kTiles == 2) load(&map_v, g);
+                else if (j > 0) load(&map_v, g_prev);
+                g_prev = g;
+                g = g_next;
+            }
+            if (kTiles == 1) load(&map_v, g_prev);
+        } while (W.next(a));
+    } else if (warp == 1) {
+        // ---- MMA: one thread issues, in the order of the ring ----
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
+            constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
+            uint32_t seq = 0, tile[2] = {0, 0}, seg[2] = {0, 0};   // ring position; per row tile: key tiles, units
+            auto stage_wait = [&](uint32_t s) {
+                wait_bar(&S.full[s % C::kStages], (s / C::kStages) & 1, S, a.flags);
+                tmem_fence_after_sync();
+                return smem_u32(ring + (s % C::kStages) * C::kStage);
+            };
+            auto issue_s = [&](int w, uint32_t buf, uint32_t kaddr) {
+                const uint32_t qa = smem_u32(qs + w * C::kQTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    umma_bf16(tmem + buf * 128, umma_sdesc_sw128(qa + (k / 4) * (kRowsTile * 128) + (k % 4) * 32),
+                              umma_sdesc_sw128_sbo(kaddr + (k / 4) * 1024 + (k % 4) * 32, C::kBlocks * 1024), idesc_s, k > 0);
+                umma_commit(&S.s_full[buf]);
+            };
+            auto issue_pv = [&](int w, uint32_t buf, uint32_t vaddr, bool acc) {
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    umma_bf16_tmem_a(tmem + kOCol + w * D, tmem + buf * 128 + k * 8,
+                                     umma_sdesc_sw128_mn(vaddr + k * 2 * C::kBlocks * 1024, 1024, C::kBlocks * 1024), idesc_o,
+                                     acc || k > 0);
+                umma_commit(&S.pv_done[kTiles == 1 ? buf : (uint32_t)w]);
+            };
+            do {
+                const int nw = kTiles == 2 && W.rows(a, 1) > 0 ? 2 : 1;
+                const int n = W.nk;
+                if (kTiles == 1) {
+                    wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
+                    uint32_t kaddr = stage_wait(seq);
+                    if (aborted(S)) break;
+                    issue_s(0, tile[0] & 1, kaddr);
+                    umma_commit(&S.empty[seq % C::kStages]);
+                    ++seq;
+                    for (int j = 0; j < n; ++j) {
+                        if (j + 1 < n) {
+                            kaddr = stage_wait(seq);
+                            if (aborted(S)) break;
+                            issue_s(0, (tile[0] + 1) & 1, kaddr);
+                            umma_commit(&S.empty[seq % C::kStages]);
+                            ++seq;
+                        }
+                        const uint32_t buf = tile[0] & 1;
+                        wait_bar(&S.p_full[buf], (tile[0] >> 1) & 1, S, a.flags);
+                        const uint32_t vaddr = stage_wait(seq);
+                        if (aborted(S)) break;
+                        issue_pv(0, buf, vaddr, j > 0);
+                        umma_commit(&S.empty[seq % C::kStages]);
+                        ++seq;
+                        ++tile[0];
+                    }
+                } else {
+                    uint32_t kaddr = stage_wait(seq);
+                    for (int w = 0; w < nw; ++w) {
+                        wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
+                        tmem_fence_after_sync();
+                        if (aborted(S)) break;
+                        issue_s(w, w, kaddr);
+                    }
+                    if (aborted(S)) break;
+                    umma_commit(&S.empty[seq % C::kStages]);
+                    for (int j = 0; j < n; ++j) {
+                        uint32_t vaddr = 0;
+                        for (int w = 0; w < nw; ++w) {
+                            wait_bar(&S.p_full[w], tile[w] & 1, S, a.flags);
+                            ++tile[w];
+                            if (w == 0) vaddr = stage_wait(seq + 1);
+                            tmem_fence_after_sync();
+                            if (aborted(S)) break;
+                            issue_pv(w, w, vaddr, j > 0);
+                            if (w == nw - 1) umma_commit(&S.empty[(seq + 1) % C::kStages]);
+                            if (j + 1 < n) {
+                                if (w == 0) kaddr = stage_wait(seq + 2);
+                                if (aborted(S)) break;
+                                issue_s(w, w, kaddr);
+                                if (w == nw - 1) umma_commit(&S.empty[(seq + 2) % C::kStages]);
+                            }
+                        }
+                        if (aborted(S)) break;
+                        seq += 2;
+                    }
+                }
+                if (aborted(S)) break;
+            } while (W.next(a));
+        }
+    } else {
+        // ---- softmax: warpgroup w owns row tile w, thread = row = TMEM lane ----
+        const int w = (warp - 2) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const int qwarp = (warp - 2) & 3;             // this warp's share of the query copy
+        unsigned char* q_dst = qs + w * C::kQTile;
+        const float c = a.scale * 1.4426950408889634f;   // scores to powers of two
+        uint32_t seq = 0, tile = 0;
+        // The product of this row tile's key tile t is in O.  A wait tells two
+        // phases of its barrier apart, so each must find the phase before its
+        // own complete.  With one row tile that is only known of t - 2 (its
+        // product precedes S of t; t - 1's may still wait for its values), so
+        // even and odd tiles have barriers of their own.
+        auto wait_pv = [&](uint32_t t) {
+            if (kTiles == 1) wait_bar(&S.pv_done[t & 1], (t >> 1) & 1, S, a.flags);
+            else wait_bar(&S.pv_done[w], t & 1, S, a.flags);
+        };
+
+        // the unit's queries, rows of 128 bytes per 64 components, swizzled
+        auto load_q = [&](const Walk<C::kRows>& U, int rows) {
+            constexpr int kLanes = D / 8;               // lanes per row, 16 bytes each
+            constexpr int kPer = 32 / kLanes;           // rows per warp and step
+            const int ch = lane % kLanes;
+            for (int r0 = qwarp * kPer + lane / kLanes; r0 < rows; r0 += 4 * kPer) {
+                const int gr = U.rt * C::kRows + w * kRowsTile + r0;
+                const int tok = U.q.t0 + gr / group, hd = U.h * group + gr % group;
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_tok + hd * a.q_head + ch * 8));
+                *reinterpret_cast<uint4*>(q_dst + (ch >> 3) * (kRowsTile * 128) + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4)) = x;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_full[w]);
+        };
+
+        int rows = W.rows(a, w);
+        if (rows > 0) load_q(W, rows);
+        bool more = true;
+        while (more) {
+            const Walk<C::kRows> U = W;
+            const int nr = rows;
+            const int n = U.q.n, len = U.q.ctx + n;
+            const bool both = kTiles == 2 && U.rows(a, 1) > 0;
+            if (nr == 0) {   // this warpgroup has no rows in the unit
+                seq += 2 * U.nk;
+                more = W.next(a);
+                if (more) {
+                    rows = W.rows(a, w);
+                    if (rows > 0) load_q(W, rows);
+                }
+                continue;
+            }
+            const bool live = quad * 32 < nr;          // this warp has rows
+            const bool valid = row < nr;
+            const int gr = U.rt * C::kRows + w * kRowsTile + (valid ? row : 0);
+            const int ti = gr / group;                 // token within the request
+            const uint32_t* mrow = a.mask ? a.mask + (size_t)(U.q.t0 + ti) * a.mask_words : nullptr;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < U.nk; ++j) {
+                const uint32_t buf = kTiles == 1 ? (tile & 1) : (uint32_t)w;
+                const uint32_t sph = kTiles == 1 ? (tile >> 1) & 1 : tile & 1;
+                const int k0 = (U.kt + j) * kKeys;
+                const bool masked = k0 + kKeys > U.q.ctx;
+                uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+                float poison = 0.f;
+                if (masked) {
+                    // value rows past the context: zero those past the length, and those that are not finite
+                    const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
+                    wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
+                    unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (row >> 3) * (C::kBlocks * 1024) + (row & 7) * 128;
+                    bool bad = false;
+                    if (k0 + row >= U.q.ctx && k0 + row < len)
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + ((x & 7) << 4));
+                            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                bad |= (q4[y] & 0x7f80u) == 0x7f80u || (q4[y] & 0x7f800000u) == 0x7f800000u;
+                        }
+                    const uint32_t badw = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) S.bad[w][tile & 1][quad] = badw;   // the other parity may still be read
+                    // all have looked before anyone zeroes
+                    if (both) named_barrier(1, 256); else named_barrier(2 + w, 128);
+                    if (w == 0 && (bad || k0 + row >= len))
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        bits[x] = seen_bits(mrow, a.mask_words, ti, n, k0 + 32 * x - U.q.ctx);
+                        if (bits[x] & S.bad[w][tile & 1][x]) poison = NAN;
+                    }
+                }
+                wait_bar(&S.s_full[buf], sph, S, a.flags);
+                tmem_fence_after_sync();
+                if (live) {
+                    uint32_t s[128];
+                    tmem_ld128(lanes + buf * 128, s);
+                    if (masked) {
+#pragma unroll
+                        for (int x = 0; x < 128; ++x)
+                            if (!((bits[x >> 5] >> (x & 31)) & 1u)) s[x] = 0xff800000u;   // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (j == 0) {
+                        m = mt;
+                    } else {
+                        const bool grow = m == -INFINITY ? mt > -INFINITY : (mt - m) * c > kLazy;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            // the previous tile's product has to be in O before it is corrected
+                            const float mn = fmaxf(m, mt), f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+                            wait_pv(tile - 1);
+                            tmem_fence_after_sync();
+#pragma unroll
+                            for (int x = 0; x < D / 32; ++x) {
+                                uint32_t o[32];
+                                tmem_ld32(lanes + kOCol + w * D + x * 32, o);
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                                tmem_st32(lanes + kOCol + w * D + x * 32, o);
+                            }
+                            l *= f;
+                            m = mn;
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : -m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) {
+                        const float p0 = ex2(fmaf(__uint_as_float(s[2 * x]), c, off));
+                        const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + 1]), c, off));
+                        sum[(2 * x) & 3] += p0;
+                        sum[(2 * x + 1) & 3] += p1;
+                        const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+                        s[x] = *reinterpret_cast<const uint32_t*>(&p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]) + poison;
+                    tmem_st32(lanes + buf * 128, s);
+                    tmem_st32(lanes + buf * 128 + 32, s + 32);
+                    tmem_wait_st();
+                }
+                tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.p_full[buf]);
+                ++tile;
+            }
+            seq += 2 * U.nk;
+            // the next unit's queries, while the last product runs
+            more = W.next(a);
+            if (more) {
+                rows = W.rows(a, w);
+                if (rows > 0) load_q(W, rows);
+            }
+            // ---- the unit's result, or its part ----
+            wait_pv(tile - 1);
+            tmem_fence_after_sync();
+            if (live) {
+                const bool whole = U.nk == U.q.nkt;
+                const size_t orow = (size_t)(U.q.t0 + ti) * a.heads + U.h * group + gr % group;
+                const int slot = 2 * blockIdx.x + (U.first ? 0 : 1);
+                const size_t prow = (size_t)slot * a.rows + w * kRowsTile + row;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    __syncwarp();   // the load is the whole warp's
+                    tmem_ld32(lanes + kOCol + w * D + x * 32, o);
+                    if (whole && valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + x * 32);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(
+                                    l == 0.f ? 0.f : __uint_as_float(o[8 * y + 2 * z]) * inv,
+                                    l == 0.f ? 0.f : __uint_as_float(o[8 * y + 2 * z + 1]) * inv);
+                                v[z] = *reinterpret_cast<const uint32_t*>(&p);
+                            }
+                            dst[y] = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else if (valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.o + prow * D + x * 32);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                }
+                if (valid) {
+                    if (!whole) a.ml[prow] = make_float2(m * c, l);
+                    else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+                }
+                tmem_fence_before_sync();   // read before the next unit's product overwrites O
+            }
+        }
+    }
+    if (aborted(S)) {   // copies that no MMA waited for land before the shared memory is released
+        const long long t0 = clock64();
+        while (clock64() - t0 < 40000) __nanosleep(1000);
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tmem_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the units that the ranges' ends cut: block x takes the
+// unit that range x + 1 starts inside of, unless an earlier range does too;
+// a warp per row adds the parts in the order of the ranges.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionArgs a, int grid, int unit_rows) {
+    grid_dependency_wait();
+    const long long total = *a.total;
+    const int ranges = (int)min((long long)grid, total);
+    const int c = blockIdx.x + 1;
+    if (c >= ranges) return;
+    const RangeStart rec = a.plan[c];
+    auto start = [&](int x) { return total * x / ranges; };
+    const long long at = start(c), u0 = at - rec.kt, u1 = u0 + rec.nkt;   // the unit's stretch of the line
+    if (rec.kt == 0 || start(c - 1) > u0) return;
+    const int group = a.heads / a.kv_heads;
+    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int gr = rec.rt * unit_rows + row;
+    if (row >= unit_rows || gr >= rec.n * group) return;
+    const int first = c - 1, last = (int)((u1 * ranges - 1) / total);    // ranges with a part
+    const int slot0 = 2 * first + (start(first) >= u0 ? 0 : 1);
+    auto index = [&](int x) { return (size_t)(x == first ? slot0 : 2 * x) * a.rows + row; };
+    float mx = -INFINITY;
+    for (int x = first + lane; x <= last; x += 32) mx = fmaxf(mx, a.ml[index(x)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    constexpr int kPer = D / 32;
+    float o[kPer], l = 0.f;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) o[y] = 0.f;
+    for (int x0 = first; x0 <= last; x0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (x0 + lane <= last) ml = a.ml[index(x0 + lane)];
+        const float wl = ml.x == -INFINITY && mx == -INFINITY ? 0.f : ex2(ml.x - mx);
+        const float ll = ml.y * wl;
+        const int n = min(32, last - x0 + 1);
+#pragma unroll 4
+        for (int x = 0; x < n; ++x) {
+            const float f = __shfl_sync(0xffffffffu, wl, x);
+            l += __shfl_sync(0xffffffffu, ll, x);
+            const float* src = a.o + index(x0 + x) * D + lane * kPer;
+            if (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
+                o[kPer - 2] = fmaf(f, v.z, o[kPer - 2]); o[kPer - 1] = fmaf(f, v.w, o[kPer - 1]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
+            }
+        }
+    }
+    const size_t orow = (size_t)(rec.t0 + gr / group) * a.heads + rec.h * group + gr % group;
+    const float inv = 1.f / l;
+    uint32_t v[kPer / 2];
+#pragma unroll
+    for (int y = 0; y < kPer / 2; ++y) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(l == 0.f ? 0.f : o[2 * y] * inv, l == 0.f ? 0.f : o[2 * y + 1] * inv);
+        v[y] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int y = 0; y < kPer / 2; ++y) dst[y] = v[y];
+    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+}
+
+// The cache seen as 8-row groups of swizzle atoms: {64 components, 8 rows,
+// blocks of 64, groups}; one box is a page's rows of one key head (or 128).
+bool encode_cache(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 enc, const void* base, int D, long long rows, int box_rows) {
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)(D / 64), (cuuint64_t)(rows / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(box_rows / 8)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int kTiles>
+cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
+    using C = Cfg<D, kTiles>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        e = cudaFuncSetAttribute(attention_tc_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<D, kTiles>, a, mk, mv);
+    if (e != cudaSuccess) return e;
+    // a unit of one key tile is never cut
+    if ((long long)a.max_pages * a.page_size <= kKeys || grid < 2) return cudaSuccess;
+    const int rows = a.rows < C::kRows ? a.rows : C::kRows;
+    cfg.gridDim = dim3(grid - 1, (rows + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, a, grid, (int)C::kRows);
+}
+
+}  // namespace
+
+bool attention_tc_supported(const AttentionArgs& a, int dtype) {
+    if (dtype != MOE_DTYPE_BF16 || (a.D != 64 && a.D != 128)) return false;
+    // whole swizzle atoms, and pages that a tile of keys holds whole or lies inside of
+    if (a.page_size % 8 != 0 || (kKeys % a.page_size != 0 && a.page_size % kKeys != 0)) return false;
+    return a.n_pages > 0 && (long long)a.n_pages * a.kv_heads * a.page_size / 8 < 0x7fffffffLL;
+}
+
+cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s) {
+    const auto enc = tensor_map_encoder();
+    if (!enc || sms <= 0) return cudaErrorNotSupported;
+    const int grid = sms < kAttentionRanges ? sms : kAttentionRanges;
+    const long long rows = (long long)a.n_pages * a.kv_heads * a.page_size;
+    CUtensorMap mk, mv;
+    const int box = a.page_size < kKeys ? a.page_size : kKeys;
+    if (!encode_cache(&mk, enc, a.ck, a.D, rows, box) || !encode_cache(&mv, enc, a.cv, a.D, rows, box))
+        return cudaErrorInvalidValue;
+    // Two row tiles a unit where the requests have more than 128 rows a key
+    // head on average: their keys and values are then read once, not twice.
+    const bool two = (long long)a.T * (a.heads / a.kv_heads) > 128LL * a.R;
+    if (a.D == 128) return two ? launch_t<128, 2>(a, mk, mv, grid, s) : launch_t<128, 1>(a, mk, mv, grid, s);
+    return two ? launch_t<64, 2>(a, mk, mv, grid, s) : launch_t<64, 1>(a, mk, mv, grid, s);
+}
+
+}  // namespace moe

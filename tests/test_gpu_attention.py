@@ -312,3 +312,21 @@ def test_long_context_many_splits():
     a = Case([9999], [1], 8, 1, 128, 64, "f32", False, 19)
     whole, lw, _ = a.run()
     a.check(whole, lw)
+
+
+@pytest.mark.parametrize("R,most,n,H,K,D,page,dtype", [
+    (90, 3500, 1, 32, 4, 128, 16, "bf16"), (40, 2500, 9, 32, 4, 128, 16, "bf16"), (25, 2000, 40, 16, 2, 128, 64, "bf16"),
+    (200, 150, 2, 16, 4, 128, 16, "bf16"), (70, 3000, 2, 32, 4, 64, 32, "bf16"), (30, 1500, 33, 32, 4, 64, 8, "bf16"),
+    (300, 60, 1, 8, 8, 128, 128, "bf16"), (60, 900, 3, 8, 2, 64, 16, "f32")])
+def test_many_requests(R, most, n, H, K, D, page, dtype):
+    """More units than blocks: a block goes through several units and parts of units, all with the same bits again."""
+    g = torch.Generator().manual_seed(R)
+    ctx = torch.randint(0, most + 1, (R,), generator=g).tolist()
+    ns = torch.randint(0 if n > 1 else 1, n + 1, (R,), generator=g).tolist()
+    c = Case(ctx, ns, H, K, D, page, dtype, n > 1, R + 1)
+    out, l, flags = c.run()
+    assert flags == 0
+    c.check(out, l)
+    for _ in range(5):
+        out2, l2, _ = c.run()
+        assert torch.equal(out, out2) and torch.equal(l, l2)
