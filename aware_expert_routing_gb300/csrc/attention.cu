@@ -20,7 +20,7 @@ constexpr int kSimpleWarps = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kSimpleWarps * 32) attention_simple_kernel(AttentionArgs a) {
-    const int t = blockIdx.x, h = blockIdx.y, kh = h / (a.heads / a.kv_heads);
+    const int t = blockIdx.x, h = blockIdx.y, kh = h / a.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ float sm[kSimpleWarps], sl[kSimpleWarps], so[kSimpleWarps][MOE_MAX_HEAD_DIM];
     // the token's request: the last r with q_offsets[r] <= t
@@ -147,7 +147,7 @@ moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int
     a.q = q; a.q_offsets = q_offsets; a.ctx_len = ctx_len; a.mask = mask;
     a.ck = cache->k; a.cv = cache->v; a.page_table = cache->page_table;
     a.out = out; a.lse = lse; a.flags = &static_cast<WsHeader*>(workspace)->flags;
-    a.T = p->T; a.heads = p->heads; a.kv_heads = cache->kv_heads; a.D = cache->head_dim; a.R = cache->n_requests;
+    a.T = p->T; a.heads = p->heads; a.kv_heads = cache->kv_heads; a.group = p->heads / cache->kv_heads; a.D = cache->head_dim; a.R = cache->n_requests;
     a.n_pages = cache->n_pages; a.page_size = cache->page_size; a.max_pages = cache->max_pages;
     a.mask_words = mask ? p->mask_words : 0;
     a.scale = p->scale; a.q_tok = p->q_tok; a.q_head = p->q_head;

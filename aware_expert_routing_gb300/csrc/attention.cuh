@@ -72,7 +72,7 @@ struct RangeStart {
 inline AttentionLayout attention_layout(int T, int group, int D) {
     AttentionLayout L;
     const long long rows = (long long)T * group;
-    L.rows = (int)(rows < kAttentionRows ? rows : kAttentionRows);
+    L.rows = (int)(rows < kAttentionRows ? (rows + 31) / 32 * 32 : kAttentionRows);   // whole warps
     size_t o = align256(MOE_ATTENTION_WORKSPACE_MIN);
     L.plan = o; o += align256(16 + sizeof(RangeStart) * kAttentionRanges);
     L.ml = o;   o += align256(sizeof(float2) * 2 * kAttentionRanges * (size_t)L.rows);
@@ -103,7 +103,7 @@ struct AttentionArgs {
     void* out;                 // [T][heads][D]
     float* lse;                // [T][heads] or null
     uint32_t* flags;
-    int T, heads, kv_heads, D, R, n_pages, page_size, max_pages, mask_words;
+    int T, heads, kv_heads, group, D, R, n_pages, page_size, max_pages, mask_words;   // group: heads / kv_heads
     float scale;
     long long q_tok, q_head;
     // tensor-core kernel: its part of the workspace (AttentionLayout)

@@ -36,6 +36,8 @@
 //     NaN through l, the others are not touched.
 #include <cudaTypedefs.h>
 
+#include <cstddef>
+
 #include "attention.cuh"
 
 namespace moe {
@@ -129,16 +131,61 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Descriptor of an MN-major operand in 128-byte swizzle atoms of 8 K-rows by
-// 64 elements: atoms `lbo` bytes apart along MN and `sbo` along K.
-__device__ __forceinline__ uint64_t umma_sdesc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The MMA warp runs its loop as a whole, so that addresses and descriptors
+// stay in uniform registers (issued from one thread's branch, every operand of
+// every MMA is moved there first: 150 cycles an MMA, measured, against 64 for
+// its work); an elected lane issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+        ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 template <int D, int kTiles>
 struct Cfg {
-    static constexpr int kThreads = 64 + 128 * kTiles;
+    // warps 0 and 1 copy and issue MMAs, the softmax's warpgroups follow; two
+    // of those start at a warpgroup's boundary, so that registers can be moved
+    // to them from the first one
+    static constexpr int kFirst = kTiles == 1 ? 2 : 4;
+    static constexpr int kThreads = 32 * kFirst + 128 * kTiles;
     static constexpr int kBlocks = D / 64;              // 64-component blocks of a head
     static constexpr int kStage = kKeys * D * 2;        // a tile of keys or of values
     static constexpr int kQTile = kRowsTile * D * 2;
@@ -162,6 +209,9 @@ static_assert(sizeof(Control) <= 2048, "control block");
 
 __device__ __forceinline__ bool aborted(Control& S) { return *(volatile int*)&S.abort_flag != 0; }
 
+// The same for a whole warp that stays together.
+__device__ __forceinline__ bool warp_aborted(Control& S) { return __any_sync(0xffffffffu, aborted(S)); }
+
 // Bounded mbarrier wait; once the CTA has given up every later wait returns
 // at once, so the control flow (and every barrier) still completes.
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Control& S, uint32_t* flags) {
@@ -177,6 +227,21 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Control
     }
 }
 
+// The line of `total` key tiles in `ranges` equal stretches (the first ones a
+// tile longer where it does not divide).
+struct Line {
+    long long q, rem;
+    __device__ __forceinline__ Line(long long total, int ranges) {
+        q = ranges > 0 ? total / ranges : 0;
+        rem = total - q * ranges;
+    }
+    __device__ __forceinline__ long long start(int c) const { return q * c + min((long long)c, rem); }
+    __device__ __forceinline__ int range_of(long long x) const {   // q > 0
+        const long long cut = rem * (q + 1);
+        return x < cut ? (int)(x / (q + 1)) : (int)(rem + (x - cut) / q);
+    }
+};
+
 struct Request {
     int t0, n, ctx, nrt, nkt;   // n 0: nothing to do
 };
@@ -191,7 +256,7 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, b
     bad = q.t0 < 0 || t1 > a.T || t1 < q.t0 ||
           (q.n > 0 && (q.ctx < 0 || (long long)q.ctx + q.n > (long long)a.max_pages * a.page_size));
     if (bad) q.n = 0;
-    q.nrt = (q.n * (a.heads / a.kv_heads) + kRows - 1) / kRows;
+    q.nrt = (q.n * a.group + kRows - 1) / kRows;
     q.nkt = q.n > 0 ? (q.ctx + q.n + kKeys - 1) / kKeys : 0;
     return q;
 }
@@ -239,23 +304,28 @@ struct Walk {
     }
     // rows of row tile w of this unit
     __device__ __forceinline__ int rows(const AttentionArgs& a, int w) const {
-        return max(0, min(kRowsTile, q.n * (a.heads / a.kv_heads) - rt * kRows - w * kRowsTile));
+        return max(0, min(kRowsTile, q.n * a.group - rt * kRows - w * kRowsTile));
     }
 };
 
-// Bits d0 .. d0 + 31 of what token i of n sees among the drafted tokens
-// (negative ones are the context).
-__device__ __forceinline__ uint32_t seen_bits(const uint32_t* mrow, int words, int i, int n, int d0) {
-    if (d0 <= -32) return 0xffffffffu;
+// Bits d0 .. d0 + 127 of what token i of n sees among the drafted tokens
+// (negative ones are the context): five words, shifted into four.
+__device__ __forceinline__ void seen_bits(const uint32_t* mrow, int words, int i, int n, int d0, uint32_t (&bits)[4]) {
     const int lim = mrow ? n : min(n, i + 1);
-    auto word = [&](int w) -> uint32_t {
-        uint32_t m = mrow ? (w < words ? mrow[w] : 0u) : 0xffffffffu;
-        const int k = lim - 32 * w;
-        return k <= 0 ? 0u : k < 32 ? m & ((1u << k) - 1u) : m;
-    };
-    if (d0 < 0) return ((1u << -d0) - 1u) | (word(0) << -d0);
-    const int w = d0 >> 5, sh = d0 & 31;
-    return sh ? __funnelshift_r(word(w), word(w + 1), sh) : word(w);
+    const int w0 = d0 >> 5;   // rounds down
+    uint32_t v[5];
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+        const int w = w0 + x;
+        v[x] = w < 0 || !mrow ? 0xffffffffu : w < words ? __ldg(mrow + w) : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+        const int k = lim - 32 * (w0 + x);
+        if (w0 + x >= 0) v[x] = k <= 0 ? 0u : k < 32 ? v[x] & ((1u << k) - 1u) : v[x];
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) bits[x] = __funnelshift_r(v[x], v[x + 1], d0 & 31);
 }
 
 template <int D, int kTiles>
@@ -268,7 +338,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
     unsigned char* qs = smem + C::kStages * C::kStage;          // [kTiles][kQTile]
     Control& S = *reinterpret_cast<Control*>(qs + kTiles * C::kQTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = a.heads / a.kv_heads;
+    const int group = a.group;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -315,16 +385,17 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             if (w < warp) before += S.scan[w];
             total += S.scan[w];
         }
-        const long long ranges = min((long long)gridDim.x, total);
-        const long long b = ranges > 0 ? total * blockIdx.x / ranges : 0, e = ranges > 0 ? total * (blockIdx.x + 1) / ranges : 0;
+        const int ranges = (int)min((long long)gridDim.x, total);
+        const Line line(total, ranges);
+        const long long b = line.start(blockIdx.x), e = line.start(blockIdx.x + 1);
         before += inc - sum;
         if (threadIdx.x == 0) {
-            const bool mine = blockIdx.x < ranges;
+            const bool mine = (int)blockIdx.x < ranges;
             S.begin = mine ? b : 0;
             S.end = mine ? e : 0;
             if (blockIdx.x == 0) *a.total = total;
         }
-        if (blockIdx.x < ranges && b >= before && b < before + sum) {
+        if ((int)blockIdx.x < ranges && b >= before && b < before + sum) {
             long long at = before;
             for (int r = r0; r < r1; ++r) {
                 bool bad;
@@ -357,19 +428,22 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         // no work for this CTA
     } else if (warp == 0) {
         // ---- producer: pages into the ring, in the order in which the MMAs read them ----
+        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         uint32_t seq = 0;
         const int page = a.page_size;
         const int per = page < kKeys ? kKeys / page : 1;        // pages of a tile
         const int prow = page < kKeys ? page : kKeys;           // rows of a copy
         const uint32_t bytes = (uint32_t)prow * D * 2;
+        const int batch = 32 / per;                             // tiles whose table entries the warp reads at once
+        const int my_tile = lane / per, my_page = lane - my_tile * per;
         do {
             const int len = W.q.ctx + W.q.n;
             const int32_t* table = a.page_table + (size_t)W.r * a.max_pages;
-            // lane i: first 8-row group of copy i of tile j (or -1)
-            auto group_of = [&](int j) -> int {
-                const int pos = (W.kt + j) * kKeys + lane * prow;
-                if (j >= W.nk || lane >= per || pos >= len) return -1;
-                int id = table[pos / page];
+            // this lane's page of the batch from tile j on: its first 8-row group, or -1
+            auto read = [&](int j) -> int {
+                const int pos = (W.kt + j + my_tile) * kKeys + my_page * prow;
+                if (j + my_tile >= W.nk || my_tile >= batch || pos >= len) return -1;
+                int id = __ldg(table + pos / page);
                 if (id < 0 || id >= a.n_pages) {
                     raise_flag(a.flags, kFlagBadIndex);
                     id = 0;
@@ -381,116 +455,142 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 wait_bar(&S.empty[st], ph ^ 1, S, a.flags);
                 ++seq;
                 const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
-                if (aborted(S)) return;
+                if (warp_aborted(S)) return;
                 if (lane == 0) mbar_arrive_expect_tx(&S.full[st], n * bytes);
                 __syncwarp();
                 if (g >= 0) tma_load_4d(smem_u32(ring + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &S.full[st]);
             };
-            int g_prev = -1, g = group_of(0);
+            int cur = read(0), nxt = read(batch), g_prev = -1, at = 0;
             for (int j = 0; j < W.nk; ++j) {
-                const int g_next = group_of(j + 1);
+                const int t = __shfl_sync(0xffffffffu, cur, min(31, at * per + lane));
+                const int g = lane < per ? t : -1;
                 load(&map_k, g);
                 if (kTiles == 2) load(&map_v, g);
                 else if (j > 0) load(&map_v, g_prev);
                 g_prev = g;
-                g = g_next;
+                if (++at == batch) {
+                    at = 0;
+                    cur = nxt;
+                    nxt = read(j + 1 + batch);
+                }
             }
             if (kTiles == 1) load(&map_v, g_prev);
         } while (W.next(a));
     } else if (warp == 1) {
         // ---- MMA: one thread issues, in the order of the ring ----
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
-            constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
-            uint32_t seq = 0, tile[2] = {0, 0}, seg[2] = {0, 0};   // ring position; per row tile: key tiles, units
-            auto stage_wait = [&](uint32_t s) {
-                wait_bar(&S.full[s % C::kStages], (s / C::kStages) & 1, S, a.flags);
-                tmem_fence_after_sync();
-                return smem_u32(ring + (s % C::kStages) * C::kStage);
-            };
-            auto issue_s = [&](int w, uint32_t buf, uint32_t kaddr) {
-                const uint32_t qa = smem_u32(qs + w * C::kQTile);
+        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
+        constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
+        const uint32_t ctl = uniform(smem_u32(&S)), ring0 = uniform(smem_u32(ring)), q0 = uniform(smem_u32(qs)), tm = uniform(tmem);
+        uint32_t st = 0, ph = 0;                        // next stage of the ring, its phase
+        uint32_t tile[2] = {0, 0}, seg[2] = {0, 0};     // per row tile: key tiles, units
+        // waits for the next stage; its shared memory address
+        auto stage_wait = [&](uint32_t s_, uint32_t p_) {
+            wait_bar(&S.full[s_], p_, S, a.flags);
+            tmem_fence_after_sync();
+            return ring0 + s_ * C::kStage;
+        };
+        auto advance = [&]() {
+            if (++st == C::kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        };
+        // Shared-memory descriptors: a constant part, and the address in the
+        // low word.  Q and K are K-major, 8-row groups 1024 and kBlocks * 1024
+        // bytes apart.  V is MN-major: swizzle atoms of 8 keys by 64
+        // components, 1024 bytes apart along the components (leading offset)
+        // and kBlocks * 1024 along the keys (stride offset).
+        constexpr uint64_t q_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(1024 >> 4) << 32 | 1u << 16;
+        constexpr uint64_t k_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | 1u << 16;
+        constexpr uint64_t v_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | (1024u >> 4) << 16;
+        auto issue_s = [&](int w, uint32_t buf, uint32_t kaddr) {
+            const uint32_t qa = (q0 + w * C::kQTile) >> 4, ka = kaddr >> 4, d = tm + buf * 128;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    umma_bf16(tmem + buf * 128, umma_sdesc_sw128(qa + (k / 4) * (kRowsTile * 128) + (k % 4) * 32),
-                              umma_sdesc_sw128_sbo(kaddr + (k / 4) * 1024 + (k % 4) * 32, C::kBlocks * 1024), idesc_s, k > 0);
-                umma_commit(&S.s_full[buf]);
-            };
-            auto issue_pv = [&](int w, uint32_t buf, uint32_t vaddr, bool acc) {
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss(d, q_hi | (qa + ((k / 4) * (kRowsTile * 128) + (k % 4) * 32) / 16),
+                       k_hi | (ka + ((k / 4) * 1024 + (k % 4) * 32) / 16), idesc_s, k > 0);
+            mma_commit(ctl + (uint32_t)offsetof(Control, s_full) + 8 * (buf));
+        };
+        auto issue_pv = [&](int w, uint32_t buf, uint32_t vaddr, uint32_t acc) {
+            const uint32_t va = vaddr >> 4, d = tm + kOCol + w * D, p = tm + buf * 128;
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    umma_bf16_tmem_a(tmem + kOCol + w * D, tmem + buf * 128 + k * 8,
-                                     umma_sdesc_sw128_mn(vaddr + k * 2 * C::kBlocks * 1024, 1024, C::kBlocks * 1024), idesc_o,
-                                     acc || k > 0);
-                umma_commit(&S.pv_done[kTiles == 1 ? buf : (uint32_t)w]);
-            };
-            do {
-                const int nw = kTiles == 2 && W.rows(a, 1) > 0 ? 2 : 1;
-                const int n = W.nk;
-                if (kTiles == 1) {
-                    wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
-                    uint32_t kaddr = stage_wait(seq);
-                    if (aborted(S)) break;
-                    issue_s(0, tile[0] & 1, kaddr);
-                    umma_commit(&S.empty[seq % C::kStages]);
-                    ++seq;
-                    for (int j = 0; j < n; ++j) {
-                        if (j + 1 < n) {
-                            kaddr = stage_wait(seq);
-                            if (aborted(S)) break;
-                            issue_s(0, (tile[0] + 1) & 1, kaddr);
-                            umma_commit(&S.empty[seq % C::kStages]);
-                            ++seq;
-                        }
-                        const uint32_t buf = tile[0] & 1;
-                        wait_bar(&S.p_full[buf], (tile[0] >> 1) & 1, S, a.flags);
-                        const uint32_t vaddr = stage_wait(seq);
-                        if (aborted(S)) break;
-                        issue_pv(0, buf, vaddr, j > 0);
-                        umma_commit(&S.empty[seq % C::kStages]);
-                        ++seq;
-                        ++tile[0];
+            for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(d, p + k * 8, v_hi | (va + k * 2 * C::kBlocks * 1024 / 16), idesc_o, k > 0 ? 1u : acc);
+            mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
+        };
+        do {
+            const int nw = uniform(kTiles == 2 && W.rows(a, 1) > 0 ? 2 : 1);
+            const int n = uniform(W.nk);
+            if (kTiles == 1) {
+                wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
+                uint32_t kaddr = stage_wait(st, ph);
+                if (warp_aborted(S)) break;
+                issue_s(0, tile[0] & 1, kaddr);
+                mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                advance();
+                for (int j = 0; j < n; ++j) {
+                    if (j + 1 < n) {
+                        kaddr = stage_wait(st, ph);
+                        if (warp_aborted(S)) break;
+                        issue_s(0, (tile[0] + 1) & 1, kaddr);
+                        mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                        advance();
                     }
-                } else {
-                    uint32_t kaddr = stage_wait(seq);
-                    for (int w = 0; w < nw; ++w) {
-                        wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
-                        tmem_fence_after_sync();
-                        if (aborted(S)) break;
-                        issue_s(w, w, kaddr);
-                    }
-                    if (aborted(S)) break;
-                    umma_commit(&S.empty[seq % C::kStages]);
-                    for (int j = 0; j < n; ++j) {
-                        uint32_t vaddr = 0;
-                        for (int w = 0; w < nw; ++w) {
-                            wait_bar(&S.p_full[w], tile[w] & 1, S, a.flags);
-                            ++tile[w];
-                            if (w == 0) vaddr = stage_wait(seq + 1);
-                            tmem_fence_after_sync();
-                            if (aborted(S)) break;
-                            issue_pv(w, w, vaddr, j > 0);
-                            if (w == nw - 1) umma_commit(&S.empty[(seq + 1) % C::kStages]);
-                            if (j + 1 < n) {
-                                if (w == 0) kaddr = stage_wait(seq + 2);
-                                if (aborted(S)) break;
-                                issue_s(w, w, kaddr);
-                                if (w == nw - 1) umma_commit(&S.empty[(seq + 2) % C::kStages]);
-                            }
-                        }
-                        if (aborted(S)) break;
-                        seq += 2;
-                    }
+                    const uint32_t buf = tile[0] & 1;
+                    wait_bar(&S.p_full[buf], (tile[0] >> 1) & 1, S, a.flags);
+                    const uint32_t vaddr = stage_wait(st, ph);
+                    if (warp_aborted(S)) break;
+                    issue_pv(0, buf, vaddr, j > 0);
+                    mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                    advance();
+                    ++tile[0];
                 }
-                if (aborted(S)) break;
-            } while (W.next(a));
-        }
+            } else {
+                uint32_t kaddr = stage_wait(st, ph);
+                for (int w = 0; w < nw; ++w) {
+                    wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
+                    if (warp_aborted(S)) break;
+                    issue_s(w, w, kaddr);
+                }
+                if (warp_aborted(S)) break;
+                mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                advance();
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t v_st = st, v_ph = ph;
+                    advance();
+                    uint32_t vaddr = 0;
+                    for (int w = 0; w < nw; ++w) {
+                        wait_bar(&S.p_full[w], tile[w] & 1, S, a.flags);
+                        ++tile[w];
+                        if (w == 0) vaddr = stage_wait(v_st, v_ph);
+                        tmem_fence_after_sync();
+                        if (warp_aborted(S)) break;
+                        issue_pv(w, w, vaddr, j > 0);
+                        if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (v_st));
+                        if (j + 1 < n) {
+                            if (w == 0) kaddr = stage_wait(st, ph);
+                            if (warp_aborted(S)) break;
+                            issue_s(w, w, kaddr);
+                            if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                        }
+                    }
+                    if (warp_aborted(S)) break;
+                    if (j + 1 < n) advance();
+                }
+            }
+            if (warp_aborted(S)) break;
+        } while (W.next(a));
+    } else if (warp < C::kFirst) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     } else {
         // ---- softmax: warpgroup w owns row tile w, thread = row = TMEM lane ----
-        const int w = (warp - 2) >> 2, quad = warp & 3;
+        // registers: 384 x 168 at launch = 128 x 56 + 256 x 224
+        if (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int w = (warp - C::kFirst) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const int qwarp = (warp - 2) & 3;             // this warp's share of the query copy
+        const int qwarp = (warp - C::kFirst) & 3;     // this warp's share of the query copy
         unsigned char* q_dst = qs + w * C::kQTile;
         const float c = a.scale * 1.4426950408889634f;   // scores to powers of two
         uint32_t seq = 0, tile = 0;
@@ -504,24 +604,35 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             else wait_bar(&S.pv_done[w], t & 1, S, a.flags);
         };
 
-        // the unit's queries, rows of 128 bytes per 64 components, swizzled
-        auto load_q = [&](const Walk<C::kRows>& U, int rows) {
+        // A unit's queries, rows of 128 bytes per 64 components, swizzled:
+        // asynchronous copies, then their completion for the MMAs.
+        auto copy_q = [&](const Walk<C::kRows>& U, int rows) {
             constexpr int kLanes = D / 8;               // lanes per row, 16 bytes each
             constexpr int kPer = 32 / kLanes;           // rows per warp and step
             const int ch = lane % kLanes;
-            for (int r0 = qwarp * kPer + lane / kLanes; r0 < rows; r0 += 4 * kPer) {
-                const int gr = U.rt * C::kRows + w * kRowsTile + r0;
-                const int tok = U.q.t0 + gr / group, hd = U.h * group + gr % group;
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_tok + hd * a.q_head + ch * 8));
-                *reinterpret_cast<uint4*>(q_dst + (ch >> 3) * (kRowsTile * 128) + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4)) = x;
+            int r0 = qwarp * kPer + lane / kLanes;
+            const int gr = U.rt * C::kRows + w * kRowsTile + r0;
+            int tok = gr / group, g = gr - tok * group;
+            for (; r0 < rows; r0 += 4 * kPer, g += 4 * kPer) {
+                for (; g >= group; g -= group) ++tok;
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (U.q.t0 + tok) * a.q_tok + (U.h * group + g) * a.q_head + ch * 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             ::"r"(smem_u32(q_dst) + (ch >> 3) * (kRowsTile * 128) + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4)),
+                               "l"(src) : "memory");
             }
+        };
+        auto finish_q = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.q_full[w]);
         };
 
         int rows = W.rows(a, w);
-        if (rows > 0) load_q(W, rows);
+        if (rows > 0) {
+            copy_q(W, rows);
+            finish_q();
+        }
         bool more = true;
         while (more) {
             const Walk<C::kRows> U = W;
@@ -531,9 +642,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             if (nr == 0) {   // this warpgroup has no rows in the unit
                 seq += 2 * U.nk;
                 more = W.next(a);
-                if (more) {
-                    rows = W.rows(a, w);
-                    if (rows > 0) load_q(W, rows);
+                rows = more ? W.rows(a, w) : 0;
+                if (rows > 0) {
+                    copy_q(W, rows);
+                    finish_q();
                 }
                 continue;
             }
@@ -542,6 +654,9 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             const int gr = U.rt * C::kRows + w * kRowsTile + (valid ? row : 0);
             const int ti = gr / group;                 // token within the request
             const uint32_t* mrow = a.mask ? a.mask + (size_t)(U.q.t0 + ti) * a.mask_words : nullptr;
+            const size_t orow = (size_t)(U.q.t0 + ti) * a.heads + U.h * group + (gr - ti * group);
+            const bool whole = U.nk == U.q.nkt;
+            const int slot = 2 * blockIdx.x + (U.first ? 0 : 1);
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < U.nk; ++j) {
                 const uint32_t buf = kTiles == 1 ? (tile & 1) : (uint32_t)w;
@@ -551,6 +666,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
                 float poison = 0.f;
                 if (masked) {
+                    seen_bits(mrow, a.mask_words, ti, n, k0 - U.q.ctx, bits);
                     // value rows past the context: zero those past the length, and those that are not finite
                     const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
                     wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
@@ -575,13 +691,16 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        bits[x] = seen_bits(mrow, a.mask_words, ti, n, k0 + 32 * x - U.q.ctx);
+                    for (int x = 0; x < 4; ++x)
                         if (bits[x] & S.bad[w][tile & 1][x]) poison = NAN;
-                    }
                 }
                 wait_bar(&S.s_full[buf], sph, S, a.flags);
                 tmem_fence_after_sync();
+                if (j == U.nk - 1) {   // the queries have been read for the last time: the next unit's, meanwhile
+                    more = W.next(a);
+                    rows = more ? W.rows(a, w) : 0;
+                    copy_q(W, rows);
+                }
                 if (live) {
                     uint32_t s[128];
                     tmem_ld128(lanes + buf * 128, s);
@@ -616,17 +735,21 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                         }
                     }
                     const float off = m == -INFINITY ? 0.f : -m * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int x = 0; x < 64; ++x) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[2 * x]), c, off));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + 1]), c, off));
-                        sum[(2 * x) & 3] += p0;
-                        sum[(2 * x + 1) & 3] += p1;
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, off2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
                         const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
                         s[x] = *reinterpret_cast<const uint32_t*>(&p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]) + poison;
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1 + poison;
                     tmem_st32(lanes + buf * 128, s);
                     tmem_st32(lanes + buf * 128 + 32, s + 32);
                     tmem_wait_st();
@@ -637,20 +760,14 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 ++tile;
             }
             seq += 2 * U.nk;
-            // the next unit's queries, while the last product runs
-            more = W.next(a);
-            if (more) {
-                rows = W.rows(a, w);
-                if (rows > 0) load_q(W, rows);
-            }
+            if (rows > 0) finish_q();
             // ---- the unit's result, or its part ----
             wait_pv(tile - 1);
             tmem_fence_after_sync();
             if (live) {
-                const bool whole = U.nk == U.q.nkt;
-                const size_t orow = (size_t)(U.q.t0 + ti) * a.heads + U.h * group + gr % group;
-                const int slot = 2 * blockIdx.x + (U.first ? 0 : 1);
                 const size_t prow = (size_t)slot * a.rows + w * kRowsTile + row;
+                // 32 rows of a part lie side by side: [D / 4][32] float4
+                float4* part = reinterpret_cast<float4*>(a.o) + ((size_t)slot * a.rows + w * kRowsTile + quad * 32) * (D / 4) + lane;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) {
@@ -672,9 +789,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             dst[y] = make_uint4(v[0], v[1], v[2], v[3]);
                         }
                     } else if (valid) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + prow * D + x * 32);
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        for (int y = 0; y < 8; ++y)
+                            part[(x * 8 + y) * 32] = make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                                                 __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
                     }
                 }
                 if (valid) {
@@ -698,69 +816,92 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
 }
 
 // Joins the parts of the units that the ranges' ends cut: block x takes the
-// unit that range x + 1 starts inside of, unless an earlier range does too;
-// a warp per row adds the parts in the order of the ranges.
-constexpr int kJoinWarps = 8;
+// unit that range x + 1 starts inside of, unless an earlier range does too.
+// A warp holds four rows (lane: row lane % 4, components 4 (lane / 4) and on,
+// in steps of 32), and four warps share the parts of the same rows, so that
+// few parts take one round of loads; their sums meet in shared memory, always
+// in the same order.
+constexpr int kJoinRows = 8, kJoinSplit = 4, kJoinWarps = kJoinRows / 4 * kJoinSplit;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionArgs a, int grid, int unit_rows) {
+    constexpr int kSteps = D / 32;
+    __shared__ float4 so[kJoinWarps][kSteps][32];
+    __shared__ float sl[kJoinWarps][32];
     grid_dependency_wait();
     const long long total = *a.total;
     const int ranges = (int)min((long long)grid, total);
     const int c = blockIdx.x + 1;
     if (c >= ranges) return;
     const RangeStart rec = a.plan[c];
-    auto start = [&](int x) { return total * x / ranges; };
+    const Line line(total, ranges);
+    auto start = [&](int x) { return line.start(x); };
     const long long at = start(c), u0 = at - rec.kt, u1 = u0 + rec.nkt;   // the unit's stretch of the line
     if (rec.kt == 0 || start(c - 1) > u0) return;
-    const int group = a.heads / a.kv_heads;
-    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int gr = rec.rt * unit_rows + row;
-    if (row >= unit_rows || gr >= rec.n * group) return;
-    const int first = c - 1, last = (int)((u1 * ranges - 1) / total);    // ranges with a part
+    const int group = a.group;
+    const int nrows = min(unit_rows, rec.n * group - rec.rt * unit_rows);
+    if ((int)blockIdx.y * kJoinRows >= nrows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = warp % kJoinSplit;
+    const int row = blockIdx.y * kJoinRows + warp / kJoinSplit * 4 + (lane & 3), ch = lane >> 2;
+    const bool valid = row < nrows;
+    const int first = c - 1, last = line.range_of(u1 - 1);    // ranges with a part
     const int slot0 = 2 * first + (start(first) >= u0 ? 0 : 1);
-    auto index = [&](int x) { return (size_t)(x == first ? slot0 : 2 * x) * a.rows + row; };
+    auto slot = [&](int x) { return (size_t)(x == first ? slot0 : 2 * x) * a.rows; };
     float mx = -INFINITY;
-    for (int x = first + lane; x <= last; x += 32) mx = fmaxf(mx, a.ml[index(x)].x);
+    if (valid)
+        for (int x = first + ch; x <= last; x += 8) mx = fmaxf(mx, a.ml[slot(x) + row].x);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    constexpr int kPer = D / 32;
-    float o[kPer], l = 0.f;
+    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    float4 o[kSteps];
+    float l = 0.f;
 #pragma unroll
-    for (int y = 0; y < kPer; ++y) o[y] = 0.f;
-    for (int x0 = first; x0 <= last; x0 += 32) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (x0 + lane <= last) ml = a.ml[index(x0 + lane)];
-        const float wl = ml.x == -INFINITY && mx == -INFINITY ? 0.f : ex2(ml.x - mx);
-        const float ll = ml.y * wl;
-        const int n = min(32, last - x0 + 1);
+    for (int y = 0; y < kSteps; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid) {
 #pragma unroll 4
-        for (int x = 0; x < n; ++x) {
-            const float f = __shfl_sync(0xffffffffu, wl, x);
-            l += __shfl_sync(0xffffffffu, ll, x);
-            const float* src = a.o + index(x0 + x) * D + lane * kPer;
-            if (kPer == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(src);
-                o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
-                o[kPer - 2] = fmaf(f, v.z, o[kPer - 2]); o[kPer - 1] = fmaf(f, v.w, o[kPer - 1]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(src);
-                o[0] = fmaf(f, v.x, o[0]); o[1] = fmaf(f, v.y, o[1]);
+        for (int x = first + split; x <= last; x += kJoinSplit) {
+            const size_t sx = slot(x);
+            const float2 ml = a.ml[sx + row];
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
+            l = fmaf(f, ml.y, l);
+            const float4* src = reinterpret_cast<const float4*>(a.o) + (sx + (row & ~31)) * (D / 4) + ch * 32 + (row & 31);
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y) {
+                const float4 v = src[y * 256];
+                o[y].x = fmaf(f, v.x, o[y].x);
+                o[y].y = fmaf(f, v.y, o[y].y);
+                o[y].z = fmaf(f, v.z, o[y].z);
+                o[y].w = fmaf(f, v.w, o[y].w);
             }
         }
     }
-    const size_t orow = (size_t)(rec.t0 + gr / group) * a.heads + rec.h * group + gr % group;
-    const float inv = 1.f / l;
-    uint32_t v[kPer / 2];
 #pragma unroll
-    for (int y = 0; y < kPer / 2; ++y) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(l == 0.f ? 0.f : o[2 * y] * inv, l == 0.f ? 0.f : o[2 * y + 1] * inv);
-        v[y] = *reinterpret_cast<const uint32_t*>(&p);
+    for (int y = 0; y < kSteps; ++y) so[warp][y][lane] = o[y];
+    sl[warp][lane] = l;
+    __syncthreads();
+    if (split != 0 || !valid) return;
+#pragma unroll
+    for (int k = 1; k < kJoinSplit; ++k) {
+        l += sl[warp + k][lane];
+#pragma unroll
+        for (int y = 0; y < kSteps; ++y) {
+            const float4 v = so[warp + k][y][lane];
+            o[y].x += v.x;
+            o[y].y += v.y;
+            o[y].z += v.z;
+            o[y].w += v.w;
+        }
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D) + lane * (kPer / 2);
+    const int gr = rec.rt * unit_rows + row;
+    const size_t orow = (size_t)(rec.t0 + gr / group) * a.heads + rec.h * group + gr % group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int y = 0; y < kPer / 2; ++y) dst[y] = v[y];
-    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+    for (int y = 0; y < kSteps; ++y) {
+        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o[y].x * inv, o[y].y * inv);
+        const __nv_bfloat162 p1 = __floats2bfloat162_rn(o[y].z * inv, o[y].w * inv);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + y * 32 + ch * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
+    }
+    if (a.lse && ch == 0) a.lse[orow] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 // The cache seen as 8-row groups of swizzle atoms: {64 components, 8 rows,
@@ -803,7 +944,7 @@ cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtens
     // a unit of one key tile is never cut
     if ((long long)a.max_pages * a.page_size <= kKeys || grid < 2) return cudaSuccess;
     const int rows = a.rows < C::kRows ? a.rows : C::kRows;
-    cfg.gridDim = dim3(grid - 1, (rows + kJoinWarps - 1) / kJoinWarps);
+    cfg.gridDim = dim3(grid - 1, (rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, a, grid, (int)C::kRows);
@@ -829,7 +970,7 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s)
         return cudaErrorInvalidValue;
     // Two row tiles a unit where the requests have more than 128 rows a key
     // head on average: their keys and values are then read once, not twice.
-    const bool two = (long long)a.T * (a.heads / a.kv_heads) > 128LL * a.R;
+    const bool two = (long long)a.T * a.group > 128LL * a.R;
     if (a.D == 128) return two ? launch_t<128, 2>(a, mk, mv, grid, s) : launch_t<128, 1>(a, mk, mv, grid, s);
     return two ? launch_t<64, 2>(a, mk, mv, grid, s) : launch_t<64, 1>(a, mk, mv, grid, s);
 }
