@@ -1,11 +1,19 @@
-// attention.cu -- attention of a step's tokens (drafted trees, chains, single
-// tokens) to a paged cache: moe_tree_attention.
+// attention.cu -- moe_tree_attention: attention of a step's tokens (drafted
+// trees, chains, single tokens) to a paged cache.
 //
 // For token i of a request and query head h, over the positions j that it
-// sees: s_j = scale q.k_j, out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m).
-// The sums run in one pass with the running maximum m: when m grows, the sums
+// sees: s_j = scale q.k_j, out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),
+// in one pass over the keys with the running maximum m: when m grows, the sums
 // so far are multiplied by exp(m_old - m_new).
-#include "attention.cuh"
+//
+// Here: the entry point, and the kernel on CUDA cores that serves what the
+// tensor cores (attention_tc.cu) do not: fp32, and bf16 heads or pages of
+// other sizes.  fp32 has no tensor-core path that keeps fp32's accuracy, so its
+// bound is the FMA rate (74 TFLOP/s at 1.9 GHz) from about 11 query rows a key
+// head on, and the cache's bytes below.
+#include <type_traits>
+
+#include "attention_line.cuh"
 
 namespace moe {
 
@@ -13,90 +21,279 @@ int num_sms();   // api.cu
 
 namespace {
 
-// One block per (token, query head): its warps take positions in turn, a
-// lane holds components lane, lane + 32, ..., and the warps' sums are joined
-// at the end.
-constexpr int kSimpleWarps = 4;
+constexpr int kPlainCost = 2;   // a unit's own cost, in key tiles
 
-template <typename T>
-__global__ void __launch_bounds__(kSimpleWarps * 32) attention_simple_kernel(AttentionArgs a) {
-    const int t = blockIdx.x, h = blockIdx.y, kh = h / a.group;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ float sm[kSimpleWarps], sl[kSimpleWarps], so[kSimpleWarps][MOE_MAX_HEAD_DIM];
-    // the token's request: the last r with q_offsets[r] <= t
-    int lo = 0, hi = a.R;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.q_offsets[mid] <= t) lo = mid; else hi = mid;
+// kC = ceil(D / 64), kR: query rows per thread.  256 threads as 16 x 16: for
+// the scores, thread (ty, tx) has rows ty kR .. and keys tx, tx + 16, ...; for
+// the products with V, the same rows and components 4 tx .. of every 64, so a
+// row's maximum, sum and correction stay with its 16 threads (half a warp).
+// Tiles of keys and values arrive by asynchronous copies one tile ahead, in
+// the cache's own type; rows are padded by 16 bytes, which puts eight rows'
+// 16-byte words in different banks.
+template <typename T, int kC, int kR>
+struct Plain {
+    static constexpr int kRows = 16 * kR;
+    static constexpr int kKeys = kC == 1 ? 64 : 32;
+    static constexpr int kPad = 16 / (int)sizeof(T);
+    static size_t smem(int D) {
+        return 4 * (size_t)kKeys * (D + kPad) * sizeof(T) + (size_t)kRows * (D + 4) * 4 + (size_t)kRows * (kKeys + 4) * 4 +
+               2 * kKeys * sizeof(long long) + sizeof(LineStart);
     }
-    const int r = lo, t0 = a.q_offsets[r], t1 = a.q_offsets[r + 1], ctx = a.ctx_len[r];
-    if (t < t0 || t >= t1) return;
-    if (t1 > a.T || ctx < 0 || (long long)ctx + (t1 - t0) > (long long)a.max_pages * a.page_size) {
-        if (threadIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
-        return;
-    }
-    const int n = t1 - t0, i = t - t0;
-    constexpr int kPer = MOE_MAX_HEAD_DIM / 32;
-    float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-        const int x = lane + 32 * c;
-        q[c] = x < a.D ? to_float(((const T*)a.q)[t * a.q_tok + h * a.q_head + x]) : 0.f;
-        o[c] = 0.f;
-    }
-    for (int j = warp; j < ctx + n; j += kSimpleWarps) {
-        if (j >= ctx) {
-            const int d = j - ctx;
-            if (a.mask ? d >= 32 * a.mask_words || !((a.mask[(size_t)t * a.mask_words + d / 32] >> (d & 31)) & 1u) : d > i)
-                continue;
-        }
-        const int page = a.page_table[(size_t)r * a.max_pages + j / a.page_size];
-        if (page < 0 || page >= a.n_pages) {
-            if (lane == 0) raise_flag(a.flags, kFlagBadIndex);
-            continue;
-        }
-        const size_t row = (((size_t)page * a.kv_heads + kh) * a.page_size + j % a.page_size) * a.D;
-        float s = 0.f;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c)
-            if (lane + 32 * c < a.D) s = fmaf(q[c], to_float(((const T*)a.ck)[row + lane + 32 * c]), s);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        if (s == -INFINITY) continue;   // adds nothing
-        const float mn = fmaxf(m, s), old = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
-        l = l * old + p;
-#pragma unroll
-        for (int c = 0; c < kPer; ++c)
-            if (lane + 32 * c < a.D) o[c] = fmaf(o[c], old, p * to_float(((const T*)a.cv)[row + lane + 32 * c]));
-        m = mn;
-    }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) so[warp][lane + 32 * c] = o[c];
-    __syncthreads();
-    m = -INFINITY;
-    for (int w = 0; w < kSimpleWarps; ++w) m = fmaxf(m, sm[w]);
-    l = 0.f;
-    float f[kSimpleWarps];
-    for (int w = 0; w < kSimpleWarps; ++w) {
-        f[w] = sl[w] == 0.f ? 0.f : expf(sm[w] - m);
-        l += f[w] * sl[w];
-    }
-    for (int x = threadIdx.x; x < a.D; x += kSimpleWarps * 32) {
-        float v = 0.f;
-        for (int w = 0; w < kSimpleWarps; ++w) v += f[w] * so[w][x];
-        ((T*)a.out)[((size_t)t * a.heads + h) * a.D + x] = from_float<T>(l == 0.f ? 0.f : v / l);
-    }
-    if (a.lse && threadIdx.x == 0) a.lse[(size_t)t * a.heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
-cudaError_t launch_attention(const AttentionArgs& a, int dtype, cudaStream_t s) {
-    if (attention_tc_supported(a, dtype)) return launch_attention_tc(a, num_sms(), s);
-    const dim3 grid(a.T, a.heads);
-    if (dtype == MOE_DTYPE_BF16) attention_simple_kernel<__nv_bfloat16><<<grid, kSimpleWarps * 32, 0, s>>>(a);
-    else attention_simple_kernel<float><<<grid, kSimpleWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+template <typename T, int kC, int kR>
+__global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArgs a) {
+    using P = Plain<T, kC, kR>;
+    using Walk = LineWalk<P::kRows, P::kKeys, kPlainCost>;
+    constexpr int kRows = P::kRows, kKeys = P::kKeys, kJ = kKeys / 16;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    const int D = a.D, ld = D + P::kPad, group = a.group;
+    T* ks = reinterpret_cast<T*>(smem_raw);                      // [2][kKeys][ld]
+    T* vs = ks + 2 * kKeys * ld;
+    float* qs = reinterpret_cast<float*>(vs + 2 * kKeys * ld);   // [kRows][D + 4]
+    float* ps = qs + kRows * (D + 4);                            // [kRows][kKeys + 4]
+    long long* row_at = reinterpret_cast<long long*>(ps + kRows * (kKeys + 4));   // [2][kKeys]: place in the cache, -1: none
+    LineStart& S = *reinterpret_cast<LineStart*>(row_at + 2 * kKeys);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const float c = a.scale * 1.4426950408889634f;   // scores to powers of two
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+    find_start<kRows, kKeys, kPlainCost, 256>(a, S);
+    __syncthreads();
+    Walk W;
+    for (bool more = W.start(a, S); more; more = W.next(a)) {
+        const int n = W.q.n, ctx = W.q.ctx, len = ctx + n, nrows = W.rows(a), r0 = W.rt * kRows;
+        const int32_t* table = a.page_table + (size_t)W.r * a.max_pages;
+        auto locate = [&](int j) {   // the places of tile j's rows
+            if (tid < kKeys) {
+                const int pos = (W.kt + j) * kKeys + tid;
+                long long at = -1;
+                if (pos < len) {
+                    const int id = table[pos / a.page_size];
+                    if (id < 0 || id >= a.n_pages) raise_flag(a.flags, kFlagBadIndex);
+                    else at = (((long long)id * a.kv_heads + W.h) * a.page_size + pos % a.page_size) * D;
+                }
+                row_at[(j & 1) * kKeys + tid] = at;
+            }
+        };
+        auto fetch = [&](int j) {    // tile j's rows, zeros where there is none
+            const int per = D * (int)sizeof(T) / 16;
+            for (int x = tid; x < kKeys * per; x += 256) {
+                const int row = x / per, ch = x - row * per;
+                const long long at = row_at[(j & 1) * kKeys + row];
+                const size_t src = at < 0 ? 0 : (size_t)at + ch * P::kPad;
+                const int dst = ((j & 1) * kKeys + row) * ld + ch * P::kPad, bytes = at < 0 ? 0 : 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(smem_u32(ks + dst)), "l"(static_cast<const T*>(a.ck) + src), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(smem_u32(vs + dst)), "l"(static_cast<const T*>(a.cv) + src), "r"(bytes) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        locate(0);
+        for (int x = tid; x < kRows * (D / 4); x += 256) {
+            const int row = x / (D / 4), ch = x - row * (D / 4), gr = r0 + row;
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < nrows)
+                q = load4(static_cast<const T*>(a.q) + (W.q.t0 + gr / group) * a.q_tok + (W.h * group + gr % group) * a.q_head + ch * 4);
+            *reinterpret_cast<float4*>(qs + row * (D + 4) + ch * 4) = q;
+        }
+        __syncthreads();
+        fetch(0);
+
+        float m[kR], l[kR], o[kR][kC][4];
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int y = 0; y < kC; ++y)
+#pragma unroll
+                for (int z = 0; z < 4; ++z) o[i][y][z] = 0.f;
+        }
+        for (int j = 0; j < W.nk; ++j) {
+            if (j + 1 < W.nk) locate(j + 1);
+            __syncthreads();
+            if (j + 1 < W.nk) {
+                fetch(j + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncthreads();
+            // ---- scores ----
+            float s[kR][kJ];
+#pragma unroll
+            for (int i = 0; i < kR; ++i)
+#pragma unroll
+                for (int y = 0; y < kJ; ++y) s[i][y] = 0.f;
+            const T* kt = ks + (size_t)(j & 1) * kKeys * ld;
+#pragma unroll 2
+            for (int d = 0; d < D; d += 4) {
+                float4 k[kJ];
+#pragma unroll
+                for (int y = 0; y < kJ; ++y) k[y] = load4(kt + (tx + 16 * y) * ld + d);
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    const float4 q = *reinterpret_cast<const float4*>(qs + (ty * kR + i) * (D + 4) + d);
+#pragma unroll
+                    for (int y = 0; y < kJ; ++y)
+                        s[i][y] = fmaf(q.x, k[y].x, fmaf(q.y, k[y].y, fmaf(q.z, k[y].z, fmaf(q.w, k[y].w, s[i][y]))));
+                }
+            }
+            const int k0 = (W.kt + j) * kKeys;
+            const bool masked = k0 + kKeys > ctx;
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                const int gr = r0 + ty * kR + i, ti = gr / group;
+                if (masked) {
+#pragma unroll
+                    for (int y = 0; y < kJ; ++y) {
+                        const int d = k0 + tx + 16 * y - ctx;   // which drafted token; below 0: context
+                        bool seen = d < 0;
+                        if (d >= 0 && d < n && ty * kR + i < nrows)
+                            seen = a.mask ? d < 32 * a.mask_words &&
+                                                ((a.mask[(size_t)(W.q.t0 + ti) * a.mask_words + (d >> 5)] >> (d & 31)) & 1u)
+                                          : d <= ti;
+                        if (!seen) s[i][y] = -INFINITY;
+                    }
+                }
+                float mt = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < kJ; ++y) {
+                    s[i][y] *= c;
+                    mt = fmaxf(mt, s[i][y]);
+                }
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+                const float mn = fmaxf(m[i], mt);
+                const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn), sub = mn == -INFINITY ? 0.f : mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int y = 0; y < kJ; ++y) {
+                    const float p = ex2(s[i][y] - sub);
+                    sum += p;
+                    ps[(ty * kR + i) * (kKeys + 4) + tx + 16 * y] = p;
+                }
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                l[i] = l[i] * f + sum;
+                m[i] = mn;
+#pragma unroll
+                for (int y = 0; y < kC; ++y)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) o[i][y][z] *= f;
+            }
+            __syncwarp();   // a row's P is written and read by the same warp
+            // ---- O += P V; where a mask hides a value, it is not multiplied (it may be anything) ----
+            const T* vt = vs + (size_t)(j & 1) * kKeys * ld;
+            auto product = [&](auto hide) {
+#pragma unroll 2
+                for (int x = 0; x < kKeys; x += 4) {
+                    float4 p[kR];
+#pragma unroll
+                    for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(ps + (ty * kR + i) * (kKeys + 4) + x);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+#pragma unroll
+                        for (int y = 0; y < kC; ++y) {
+                            if (tx * 4 + 64 * y >= D) continue;
+                            const float4 v = load4(vt + (x + z) * ld + tx * 4 + 64 * y);
+#pragma unroll
+                            for (int i = 0; i < kR; ++i) {
+                                const float w = z == 0 ? p[i].x : z == 1 ? p[i].y : z == 2 ? p[i].z : p[i].w;
+                                if (decltype(hide)::value && w == 0.f) continue;
+                                o[i][y][0] = fmaf(w, v.x, o[i][y][0]);
+                                o[i][y][1] = fmaf(w, v.y, o[i][y][1]);
+                                o[i][y][2] = fmaf(w, v.z, o[i][y][2]);
+                                o[i][y][3] = fmaf(w, v.w, o[i][y][3]);
+                            }
+                        }
+                }
+            };
+            if (masked) product(std::true_type{});
+            else product(std::false_type{});
+        }
+        // ---- the unit's result, or its part ----
+        const bool whole = W.nk == W.q.nkt;
+        const int slot = 2 * blockIdx.x + (W.first ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            const int row = ty * kR + i, gr = r0 + row;
+            if (row >= nrows) continue;
+            const size_t orow = (size_t)(W.q.t0 + gr / group) * a.heads + W.h * group + gr % group;
+#pragma unroll
+            for (int y = 0; y < kC; ++y) {
+                if (tx * 4 + 64 * y >= D) continue;
+                const float4 v = make_float4(o[i][y][0], o[i][y][1], o[i][y][2], o[i][y][3]);
+                if (whole) store_row(static_cast<T*>(a.out) + orow * D + tx * 4 + 64 * y, v, l[i]);
+                else reinterpret_cast<float4*>(a.o)[((size_t)slot * a.rows + (row & ~31)) * (D / 4) + (tx + 16 * y) * 32 + (row & 31)] = v;
+            }
+            if (tx == 0) {
+                if (!whole) a.ml[(size_t)slot * a.rows + row] = make_float2(m[i], l[i]);
+                else if (a.lse) a.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+            }
+        }
+        __syncthreads();   // the next unit overwrites the queries and the tiles
+    }
+}
+
+template <typename T, int kC, int kR>
+cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
+    using P = Plain<T, kC, kR>;
+    const size_t smem = P::smem(a.D);
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+        e = cudaFuncSetAttribute(attention_plain_kernel<T, kC, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)P::smem(64 * kC));
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    // two blocks per SM where their shared memory allows it
+    const int want = sms * (smem <= 113 * 1024 ? 2 : 1), grid = want < kPlainRanges ? want : kPlainRanges;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, attention_plain_kernel<T, kC, kR>, a)) != cudaSuccess) return e;
+    if ((long long)a.max_pages * a.page_size <= P::kKeys || grid < 2) return cudaSuccess;   // no unit is cut
+    const int rows = a.rows < P::kRows ? a.rows : P::kRows;
+    cfg.gridDim = dim3(grid - 1, (rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, 2 * kC, kPlainCost>, a, (int)P::kRows);
+}
+
+template <typename T>
+cudaError_t launch_plain(const AttentionArgs& a, int sms, cudaStream_t s) {
+    if (sms <= 0) return cudaErrorNotSupported;
+    // units of 64 rows where the requests have more than 32 a key head on average
+    const bool tall = (long long)a.T * a.group > 32LL * a.R;
+    switch ((a.D + 63) / 64) {
+        case 1: return tall ? launch_plain_t<T, 1, 4>(a, sms, s) : launch_plain_t<T, 1, 2>(a, sms, s);
+        case 2: return tall ? launch_plain_t<T, 2, 4>(a, sms, s) : launch_plain_t<T, 2, 2>(a, sms, s);
+        case 3: return tall ? launch_plain_t<T, 3, 4>(a, sms, s) : launch_plain_t<T, 3, 2>(a, sms, s);
+        default: return tall ? launch_plain_t<T, 4, 4>(a, sms, s) : launch_plain_t<T, 4, 2>(a, sms, s);
+    }
 }
 
 }  // namespace
@@ -120,7 +317,7 @@ extern "C" {
 
 size_t moe_attention_workspace_bytes(int32_t T, int32_t heads, const moe_kv_cache* cache) {
     if (check_cache(cache, true) != MOE_OK || check_heads(T, heads, cache) != MOE_OK) return 0;
-    return attention_layout(T, heads / cache->kv_heads, cache->head_dim).total;
+    return attention_layout(T, heads / cache->kv_heads, cache->head_dim, attention_tc_fits(cache)).total;
 }
 
 moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int32_t* ctx_len, const uint32_t* mask,
@@ -136,6 +333,7 @@ moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int
     if (!workspace || !aligned(workspace, 256)) return report(MOE_ERR_WORKSPACE, "workspace is NULL or not 256-byte aligned");
     if (workspace_bytes < need) return report(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     if (p->T == 0 || cache->n_requests == 0) return MOE_OK;
+    if (cache->n_pages < 1 || cache->max_pages < 1) return report(MOE_ERR_ARG, "the cache has no pages");
     if (!q || !out || !q_offsets || !ctx_len) return report(MOE_ERR_ARG, "a tensor pointer is NULL");
     if (!aligned(q, 16) || !aligned(out, 16)) return report(MOE_ERR_ARG, "q or out is not 16-byte aligned");
     if (!aligned(q_offsets, 4) || !aligned(ctx_len, 4) || !aligned(mask, 4) || !aligned(lse, 4))
@@ -151,15 +349,19 @@ moe_status moe_tree_attention(const void* q, const int32_t* q_offsets, const int
     a.n_pages = cache->n_pages; a.page_size = cache->page_size; a.max_pages = cache->max_pages;
     a.mask_words = mask ? p->mask_words : 0;
     a.scale = p->scale; a.q_tok = p->q_tok; a.q_head = p->q_head;
-    const AttentionLayout L = attention_layout(p->T, p->heads / cache->kv_heads, cache->head_dim);
+    const bool tc = attention_tc_fits(cache);
+    const AttentionLayout L = attention_layout(p->T, p->heads / cache->kv_heads, cache->head_dim, tc);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    a.total = reinterpret_cast<long long*>(ws + L.plan);
-    a.plan = reinterpret_cast<RangeStart*>(ws + L.plan + 16);
+    a.plan = reinterpret_cast<RangeStart*>(ws + L.plan);
     a.ml = reinterpret_cast<float2*>(ws + L.ml);
     a.o = reinterpret_cast<float*>(ws + L.o);
     a.rows = L.rows;
     a.wait_cycles = wait_cycles_now();
-    const cudaError_t e = launch_attention(a, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int sms = num_sms();
+    const cudaError_t e = tc ? launch_attention_tc(a, sms, s)
+                          : cache->dtype == MOE_DTYPE_BF16 ? launch_plain<__nv_bfloat16>(a, sms, s)
+                                                           : launch_plain<float>(a, sms, s);
     return e == cudaSuccess ? MOE_OK : report(MOE_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
 }
 

@@ -41,17 +41,17 @@ inline moe_status check_cache(const moe_kv_cache* c, bool attend) {
     if (!attend) return MOE_OK;
     if (c->n_requests < 0 || c->n_requests > MOE_MAX_REQUESTS)
         return report(MOE_ERR_ARG, "n_requests=%d outside 0..%d", c->n_requests, MOE_MAX_REQUESTS);
-    if (c->max_pages < 0 || (long long)c->max_pages * c->page_size > 0x7fffffffLL)
-        return report(MOE_ERR_ARG, "max_pages=%d is negative, or positions pass 2^31 - 1", c->max_pages);
+    if (c->max_pages < 0 || (long long)c->max_pages * c->page_size > (1LL << 30))
+        return report(MOE_ERR_ARG, "max_pages=%d is negative, or positions pass 2^30", c->max_pages);
     if (c->n_requests > 0 && c->max_pages > 0 && (!c->page_table || !aligned(c->page_table, 4)))
         return report(MOE_ERR_ARG, "page_table is NULL or misaligned");
     return MOE_OK;
 }
 
-// Work of the tensor-core kernel is cut into this many equal ranges at most
-// (one per SM of a GB300), each range's ends leaving partial sums behind.
-constexpr int kAttentionRanges = 152;
-constexpr int kAttentionRows = 256;   // most query rows of a work unit
+// The tensor-core kernel: ranges of work (one per SM of a GB300) and most query
+// rows of a unit.  The other kernel: two ranges per SM.
+constexpr int kTcRanges = 152, kTcRows = 256;
+constexpr int kPlainRanges = 304, kPlainRows = 64;
 
 // Workspace of moe_tree_attention: the flag word's header, the record of each
 // range's start, and two partial results a range (of its first and its last
@@ -63,22 +63,32 @@ struct AttentionLayout {
 };
 
 struct RangeStart {
-    int t0, n;          // the request's tokens
-    int h, rt;          // key head and row tile of the unit that the range starts in
-    int kt, nkt;        // first key tile, and the unit's key tiles
-    int pad[2];
+    int t0, n;              // the request's tokens
+    int h, rt;              // key head and row tile of the unit that the range starts in
+    int off, nkt;           // steps into the unit, and the unit's key tiles (0: the range is empty)
+    int line_q, line_rem;   // how the line is cut
 };
 
-inline AttentionLayout attention_layout(int T, int group, int D) {
+inline AttentionLayout attention_layout(int T, int group, int D, bool tc) {
     AttentionLayout L;
     const long long rows = (long long)T * group;
-    L.rows = (int)(rows < kAttentionRows ? (rows + 31) / 32 * 32 : kAttentionRows);   // whole warps
+    const int most = tc ? kTcRows : kPlainRows, ranges = tc ? kTcRanges : kPlainRanges;
+    L.rows = (int)(rows < most ? (rows + 31) / 32 * 32 : most);   // whole warps
     size_t o = align256(MOE_ATTENTION_WORKSPACE_MIN);
-    L.plan = o; o += align256(16 + sizeof(RangeStart) * kAttentionRanges);
-    L.ml = o;   o += align256(sizeof(float2) * 2 * kAttentionRanges * (size_t)L.rows);
-    L.o = o;    o += align256(sizeof(float) * 2 * kAttentionRanges * (size_t)L.rows * D);
+    L.plan = o; o += align256(sizeof(RangeStart) * ranges);
+    L.ml = o;   o += align256(sizeof(float2) * 2 * ranges * (size_t)L.rows);
+    L.o = o;    o += align256(sizeof(float) * 2 * ranges * (size_t)L.rows * D);
     L.total = o;
     return L;
+}
+
+// Whether the tensor-core kernel (attention_tc.cu) takes a cache: bf16, heads
+// of 64 or 128, pages of whole 8-row swizzle atoms that a tile of 128 keys
+// holds whole or lies inside of.
+inline bool attention_tc_fits(const moe_kv_cache* c) {
+    return c->dtype == MOE_DTYPE_BF16 && (c->head_dim == 64 || c->head_dim == 128) && c->page_size % 8 == 0 &&
+           (128 % c->page_size == 0 || c->page_size % 128 == 0) &&
+           (long long)c->n_pages * c->kv_heads * c->page_size / 8 < 0x7fffffffLL;
 }
 
 struct AppendArgs {
@@ -106,17 +116,14 @@ struct AttentionArgs {
     int T, heads, kv_heads, group, D, R, n_pages, page_size, max_pages, mask_words;   // group: heads / kv_heads
     float scale;
     long long q_tok, q_head;
-    // tensor-core kernel: its part of the workspace (AttentionLayout)
-    long long* total;          // work of all requests, in key tiles
-    RangeStart* plan;          // [kAttentionRanges]
+    // the workspace (AttentionLayout)
+    RangeStart* plan;          // [ranges]
     float2* ml;                // [2 * ranges][rows]
     float* o;                  // [2 * ranges][rows][D]
     int rows;
     long long wait_cycles;
 };
 
-// Tensor-core kernel (attention_tc.cu).
-bool attention_tc_supported(const AttentionArgs& a, int dtype);
 cudaError_t launch_attention_tc(const AttentionArgs& a, int num_sms, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -14,9 +14,12 @@
 //     one another in one line with those of all other units, and each CTA (one
 //     per SM) takes an equal stretch of the line, whatever the requests'
 //     lengths.  A unit that lies in one stretch is finished there; one that is
-//     cut leaves partial (m, l, O) per stretch, which the joining kernel below
-//     adds up in the order of the stretches, so results repeat bit for bit.
-//     Lengths are read on the device: nothing depends on the host knowing them.
+//     cut leaves partial (m, l, O) per stretch, which a second kernel adds up
+//     in the order of the stretches, so results repeat bit for bit.  (Joining
+//     in this kernel, by the CTA that is last to write its part, was slower:
+//     one SM reads a unit's parts for 10 to 40 us, and even with two parts its
+//     fence and counter take as long as the second launch.)  Lengths are read
+//     on the device: nothing depends on the host knowing them.
 //   * A producer warp copies pages with TMA into a ring of key and value tiles
 //     (8-row swizzle atoms side by side, so that pages of any number of atoms
 //     make one operand), one thread issues the MMAs, and one warpgroup per row
@@ -38,7 +41,7 @@
 
 #include <cstddef>
 
-#include "attention.cuh"
+#include "attention_line.cuh"
 
 namespace moe {
 
@@ -49,6 +52,7 @@ namespace {
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kRowsTile = 128; // query rows per tile
 constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O from here
+constexpr int kUnitCost = 5;   // see attention_line.cuh; 2: 32.7, 3: 31.9, 4: 30.6, 6: 29.5 us for 16 trees of 16 to 4000
 constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
 
 // Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
@@ -114,12 +118,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -197,11 +195,9 @@ struct Cfg {
 
 struct Control {
     uint64_t full[16], empty[16], q_full[2], s_full[2], p_full[2], pv_done[2];
-    long long scan[16];
-    long long begin, end, total;
     long long wait_cycles;
-    int start_r, abort_flag;
-    long long start_off;       // key tiles of the start request before this CTA's range
+    LineStart start;
+    int abort_flag;
     uint32_t tmem_base;
     uint32_t bad[2][2][4];     // per row tile and key tile's parity: keys whose value is not finite
 };
@@ -227,97 +223,18 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, Control
     }
 }
 
-// The line of `total` key tiles in `ranges` equal stretches (the first ones a
-// tile longer where it does not divide).
-struct Line {
-    long long q, rem;
-    __device__ __forceinline__ Line(long long total, int ranges) {
-        q = ranges > 0 ? total / ranges : 0;
-        rem = total - q * ranges;
-    }
-    __device__ __forceinline__ long long start(int c) const { return q * c + min((long long)c, rem); }
-    __device__ __forceinline__ int range_of(long long x) const {   // q > 0
-        const long long cut = rem * (q + 1);
-        return x < cut ? (int)(x / (q + 1)) : (int)(rem + (x - cut) / q);
-    }
-};
-
-struct Request {
-    int t0, n, ctx, nrt, nkt;   // n 0: nothing to do
-};
-
-template <int kRows>
-__device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, bool& bad) {
-    Request q;
-    q.t0 = a.q_offsets[r];
-    const int t1 = a.q_offsets[r + 1];
-    q.ctx = a.ctx_len[r];
-    q.n = t1 - q.t0;
-    bad = q.t0 < 0 || t1 > a.T || t1 < q.t0 ||
-          (q.n > 0 && (q.ctx < 0 || (long long)q.ctx + q.n > (long long)a.max_pages * a.page_size));
-    if (bad) q.n = 0;
-    q.nrt = (q.n * a.group + kRows - 1) / kRows;
-    q.nkt = q.n > 0 ? (q.ctx + q.n + kKeys - 1) / kKeys : 0;
-    return q;
-}
-
-// A CTA's stretch of the line, one unit (or its part) at a time.
-template <int kRows>
-struct Walk {
-    Request q;
-    int r, h, rt, kt, nk;       // this part: key tiles kt .. kt + nk - 1
-    long long left;             // key tiles after this part
-    bool first;                 // the stretch's first part
-
-    __device__ __forceinline__ void part() {
-        nk = (int)min((long long)(q.nkt - kt), left);
-        left -= nk;
-    }
-    __device__ __forceinline__ void start(const AttentionArgs& a, const Control& S) {
-        bool bad;
-        r = S.start_r;
-        q = load_request<kRows>(a, r, bad);
-        const long long u = S.start_off / q.nkt;
-        kt = (int)(S.start_off - u * q.nkt);
-        h = (int)(u / q.nrt);
-        rt = (int)(u - (long long)h * q.nrt);
-        left = S.end - S.begin;
-        first = true;
-        part();
-    }
-    __device__ __forceinline__ bool next(const AttentionArgs& a) {
-        if (left <= 0) return false;
-        first = false;
-        kt = 0;
-        if (++rt >= q.nrt) {
-            rt = 0;
-            if (++h >= a.kv_heads) {
-                h = 0;
-                bool bad;
-                do q = load_request<kRows>(a, ++r, bad);
-                while (q.n == 0 && r + 1 < a.R);
-                if (q.n == 0) return false;   // not reached: the line ends with a request that has work
-            }
-        }
-        part();
-        return true;
-    }
-    // rows of row tile w of this unit
-    __device__ __forceinline__ int rows(const AttentionArgs& a, int w) const {
-        return max(0, min(kRowsTile, q.n * a.group - rt * kRows - w * kRowsTile));
-    }
-};
-
 // Bits d0 .. d0 + 127 of what token i of n sees among the drafted tokens
 // (negative ones are the context): five words, shifted into four.
-__device__ __forceinline__ void seen_bits(const uint32_t* mrow, int words, int i, int n, int d0, uint32_t (&bits)[4]) {
+// mw0 and mw1: the mask's first two words.
+__device__ __forceinline__ void seen_bits(const uint32_t* mrow, int words, uint32_t mw0, uint32_t mw1, int i, int n, int d0,
+                                          uint32_t (&bits)[4]) {
     const int lim = mrow ? n : min(n, i + 1);
     const int w0 = d0 >> 5;   // rounds down
     uint32_t v[5];
 #pragma unroll
     for (int x = 0; x < 5; ++x) {
         const int w = w0 + x;
-        v[x] = w < 0 || !mrow ? 0xffffffffu : w < words ? __ldg(mrow + w) : 0u;
+        v[x] = w < 0 || !mrow ? 0xffffffffu : w == 0 ? mw0 : w == 1 ? mw1 : w < words ? mrow[w] : 0u;
     }
 #pragma unroll
     for (int x = 0; x < 5; ++x) {
@@ -332,6 +249,7 @@ template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
 attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, kTiles>;
+    using Walk = LineWalk<C::kRows, kKeys, kUnitCost>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* ring = smem;                                 // [kStages][kStage]
@@ -339,6 +257,8 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
     Control& S = *reinterpret_cast<Control*>(qs + kTiles * C::kQTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.group;
+    // rows of row tile w of a unit
+    auto rows_of = [&](const Walk& U, int w) { return max(0, min(kRowsTile, U.rows(a) - w * kRowsTile)); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -358,71 +278,16 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         prefetch_tensormap(&map_v);
     }
     if (warp == 1) tmem_alloc(&S.tmem_base, 512);
-    grid_launch_dependents();   // the joining kernel may take its place; it waits for this grid's end
+    grid_launch_dependents();   // a kernel that follows may start its prologue; it waits for this grid's end
     grid_dependency_wait();     // lengths, queries and the cache come from preceding kernels
 
-    // ---- the line: each thread adds up a few consecutive requests -------------
-    {
-        const int per = (a.R + C::kThreads - 1) / C::kThreads;
-        const int r0 = min(a.R, (int)threadIdx.x * per), r1 = min(a.R, r0 + per);
-        long long sum = 0;
-        for (int r = r0; r < r1; ++r) {
-            bool bad;
-            const Request q = load_request<C::kRows>(a, r, bad);
-            if (bad && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
-            sum += (long long)q.nrt * q.nkt * a.kv_heads;
-        }
-        long long inc = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += t;
-        }
-        if (lane == 31) S.scan[warp] = inc;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int w = 0; w < C::kThreads / 32; ++w) {
-            if (w < warp) before += S.scan[w];
-            total += S.scan[w];
-        }
-        const int ranges = (int)min((long long)gridDim.x, total);
-        const Line line(total, ranges);
-        const long long b = line.start(blockIdx.x), e = line.start(blockIdx.x + 1);
-        before += inc - sum;
-        if (threadIdx.x == 0) {
-            const bool mine = (int)blockIdx.x < ranges;
-            S.begin = mine ? b : 0;
-            S.end = mine ? e : 0;
-            if (blockIdx.x == 0) *a.total = total;
-        }
-        if ((int)blockIdx.x < ranges && b >= before && b < before + sum) {
-            long long at = before;
-            for (int r = r0; r < r1; ++r) {
-                bool bad;
-                const Request q = load_request<C::kRows>(a, r, bad);
-                const long long w = (long long)q.nrt * q.nkt * a.kv_heads;
-                if (b < at + w) {
-                    S.start_r = r;
-                    S.start_off = b - at;
-                    break;
-                }
-                at += w;
-            }
-        }
-    }
+    find_start<C::kRows, kKeys, kUnitCost, C::kThreads>(a, S.start);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
     const uint32_t tmem = S.tmem_base;
-    const bool any = S.end > S.begin;
-    Walk<C::kRows> W;
-    if (any) W.start(a, S);
-    if (any && threadIdx.x == 0) {
-        RangeStart rec;
-        rec.t0 = W.q.t0; rec.n = W.q.n; rec.h = W.h; rec.rt = W.rt; rec.kt = W.kt; rec.nkt = W.q.nkt;
-        rec.pad[0] = rec.pad[1] = 0;
-        a.plan[blockIdx.x] = rec;
-    }
+    Walk W;
+    const bool any = W.start(a, S.start);
 
     if (!any) {
         // no work for this CTA
@@ -436,46 +301,64 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         const uint32_t bytes = (uint32_t)prow * D * 2;
         const int batch = 32 / per;                             // tiles whose table entries the warp reads at once
         const int my_tile = lane / per, my_page = lane - my_tile * per;
-        do {
-            const int len = W.q.ctx + W.q.n;
-            const int32_t* table = a.page_table + (size_t)W.r * a.max_pages;
-            // this lane's page of the batch from tile j on: its first 8-row group, or -1
-            auto read = [&](int j) -> int {
-                const int pos = (W.kt + j + my_tile) * kKeys + my_page * prow;
-                if (j + my_tile >= W.nk || my_tile >= batch || pos >= len) return -1;
-                int id = __ldg(table + pos / page);
-                if (id < 0 || id >= a.n_pages) {
-                    raise_flag(a.flags, kFlagBadIndex);
-                    id = 0;
-                }
-                return (int)((((long long)id * a.kv_heads + W.h) * page + pos % page) / 8);
-            };
-            auto load = [&](const CUtensorMap* map, int g) {
-                const uint32_t st = seq % C::kStages, ph = (seq / C::kStages) & 1;
-                wait_bar(&S.empty[st], ph ^ 1, S, a.flags);
-                ++seq;
-                const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
-                if (warp_aborted(S)) return;
-                if (lane == 0) mbar_arrive_expect_tx(&S.full[st], n * bytes);
-                __syncwarp();
-                if (g >= 0) tma_load_4d(smem_u32(ring + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &S.full[st]);
-            };
-            int cur = read(0), nxt = read(batch), g_prev = -1, at = 0;
+        const int wide = page / kKeys;                          // tiles of a page of more than 128 rows
+        // This lane's page of the batch of tiles from j on of a part: is there
+        // one, its entry in the table, and its first 8-row group in the cache
+        // (-1: no page).
+        auto has = [&](const Walk& U, int j) {
+            return my_tile < batch && j + my_tile < U.nk && (U.kt + j + my_tile) * kKeys + my_page * prow < U.q.ctx + U.q.n;
+        };
+        auto read = [&](const Walk& U, int j) -> int {
+            const int t = U.kt + j + my_tile;
+            return has(U, j) ? a.page_table[(size_t)U.r * a.max_pages + (page <= kKeys ? t * per + my_page : t / wide)] : 0;
+        };
+        auto group_of = [&](int id, int j) -> int {
+            if (!has(W, j)) return -1;
+            if (id < 0 || id >= a.n_pages) {
+                raise_flag(a.flags, kFlagBadIndex);
+                id = 0;
+            }
+            const int row = page <= kKeys ? 0 : (W.kt + j + my_tile) % wide * kKeys;
+            return (int)((((long long)id * a.kv_heads + W.h) * page + row) / 8);
+        };
+        auto load = [&](const CUtensorMap* map, int g) {
+            const uint32_t st = seq % C::kStages, ph = (seq / C::kStages) & 1;
+            wait_bar(&S.empty[st], ph ^ 1, S, a.flags);
+            ++seq;
+            const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
+            if (warp_aborted(S)) return;
+            if (lane == 0) mbar_arrive_expect_tx(&S.full[st], n * bytes);
+            __syncwarp();
+            if (g >= 0) tma_load_4d(smem_u32(ring + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &S.full[st]);
+        };
+        int id0 = read(W, 0), id1 = read(W, batch);
+        bool more = true;
+        while (more) {
+            int g_prev = -1, at = 0, cur = group_of(id0, 0), nxt = id1;
+            Walk N = W;
             for (int j = 0; j < W.nk; ++j) {
                 const int t = __shfl_sync(0xffffffffu, cur, min(31, at * per + lane));
                 const int g = lane < per ? t : -1;
                 load(&map_k, g);
                 if (kTiles == 2) load(&map_v, g);
                 else if (j > 0) load(&map_v, g_prev);
+                if (j == 0) {   // the next part's first entries, while this part is loaded
+                    more = N.next(a);
+                    if (more) {
+                        id0 = read(N, 0);
+                        id1 = read(N, batch);
+                    }
+                }
                 g_prev = g;
                 if (++at == batch) {
                     at = 0;
-                    cur = nxt;
-                    nxt = read(j + 1 + batch);
+                    cur = group_of(nxt, j + 1);
+                    nxt = read(W, j + 1 + batch);
                 }
             }
             if (kTiles == 1) load(&map_v, g_prev);
-        } while (W.next(a));
+            W = N;
+        }
     } else if (warp == 1) {
         // ---- MMA: one thread issues, in the order of the ring ----
         if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -520,7 +403,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
         };
         do {
-            const int nw = uniform(kTiles == 2 && W.rows(a, 1) > 0 ? 2 : 1);
+            const int nw = uniform(kTiles == 2 && rows_of(W, 1) > 0 ? 2 : 1);
             const int n = uniform(W.nk);
             if (kTiles == 1) {
                 wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
@@ -606,19 +489,30 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
 
         // A unit's queries, rows of 128 bytes per 64 components, swizzled:
         // asynchronous copies, then their completion for the MMAs.
-        auto copy_q = [&](const Walk<C::kRows>& U, int rows) {
-            constexpr int kLanes = D / 8;               // lanes per row, 16 bytes each
-            constexpr int kPer = 32 / kLanes;           // rows per warp and step
-            const int ch = lane % kLanes;
-            int r0 = qwarp * kPer + lane / kLanes;
-            const int gr = U.rt * C::kRows + w * kRowsTile + r0;
-            int tok = gr / group, g = gr - tok * group;
-            for (; r0 < rows; r0 += 4 * kPer, g += 4 * kPer) {
-                for (; g >= group; g -= group) ++tok;
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (U.q.t0 + tok) * a.q_tok + (U.h * group + g) * a.q_head + ch * 8;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                             ::"r"(smem_u32(q_dst) + (ch >> 3) * (kRowsTile * 128) + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4)),
-                               "l"(src) : "memory");
+        constexpr int kLanes = D / 8;               // lanes per row, 16 bytes each
+        constexpr int kPer = 32 / kLanes, kStep = 4 * kPer;   // rows per warp, and of all four at a step
+        const int ch = lane % kLanes, qrow = qwarp * kPer + lane / kLanes;
+        const uint32_t q_to = smem_u32(q_dst) + (ch >> 3) * (kRowsTile * 128) + qrow * 128 + (((ch & 7) ^ (qrow & 7)) << 4);
+        const int step_tok = kStep / group, step_g = kStep - step_tok * group;
+        const long long step = step_tok * a.q_tok + step_g * a.q_head, wrap = a.q_tok - group * a.q_head;
+        auto copy_q = [&](const Walk& U, int rows) {
+            if (qrow >= rows) return;
+            const int gr = U.rt * C::kRows + w * kRowsTile + qrow, tok = gr / group;
+            int g = gr - tok * group;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (U.q.t0 + tok) * a.q_tok +
+                                       (U.h * group + g) * a.q_head + ch * 8;
+            uint32_t to = q_to;
+            static_assert(kStep % 8 == 0, "the swizzle is the same at every step");
+#pragma unroll 4
+            for (int r0 = qrow; r0 < rows; r0 += kStep) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+                to += kStep * 128;
+                src += step;
+                g += step_g;
+                if (g >= group) {
+                    g -= group;
+                    src += wrap;
+                }
             }
         };
         auto finish_q = [&]() {
@@ -628,21 +522,21 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             if (lane == 0) mbar_arrive(&S.q_full[w]);
         };
 
-        int rows = W.rows(a, w);
+        int rows = rows_of(W, w);
         if (rows > 0) {
             copy_q(W, rows);
             finish_q();
         }
         bool more = true;
         while (more) {
-            const Walk<C::kRows> U = W;
+            const Walk U = W;
             const int nr = rows;
             const int n = U.q.n, len = U.q.ctx + n;
-            const bool both = kTiles == 2 && U.rows(a, 1) > 0;
+            const bool both = kTiles == 2 && rows_of(U, 1) > 0;
             if (nr == 0) {   // this warpgroup has no rows in the unit
                 seq += 2 * U.nk;
                 more = W.next(a);
-                rows = more ? W.rows(a, w) : 0;
+                rows = more ? rows_of(W, w) : 0;
                 if (rows > 0) {
                     copy_q(W, rows);
                     finish_q();
@@ -657,6 +551,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             const size_t orow = (size_t)(U.q.t0 + ti) * a.heads + U.h * group + (gr - ti * group);
             const bool whole = U.nk == U.q.nkt;
             const int slot = 2 * blockIdx.x + (U.first ? 0 : 1);
+            const uint32_t mw0 = mrow && a.mask_words > 0 ? mrow[0] : 0u, mw1 = mrow && a.mask_words > 1 ? mrow[1] : 0u;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < U.nk; ++j) {
                 const uint32_t buf = kTiles == 1 ? (tile & 1) : (uint32_t)w;
@@ -666,29 +561,29 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
                 float poison = 0.f;
                 if (masked) {
-                    seen_bits(mrow, a.mask_words, ti, n, k0 - U.q.ctx, bits);
+                    seen_bits(mrow, a.mask_words, mw0, mw1, ti, n, k0 - U.q.ctx, bits);
                     // value rows past the context: zero those past the length, and those that are not finite
                     const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
                     wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
                     unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (row >> 3) * (C::kBlocks * 1024) + (row & 7) * 128;
-                    bool bad = false;
+                    // (a bf16 of all-ones exponent carries into bit 15 when 0x80 is added)
+                    uint32_t top = 0;
                     if (k0 + row >= U.q.ctx && k0 + row < len)
-#pragma unroll
-                        for (int x = 0; x < D / 8; ++x) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + ((x & 7) << 4));
-                            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                bad |= (q4[y] & 0x7f80u) == 0x7f80u || (q4[y] & 0x7f800000u) == 0x7f800000u;
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {   // the swizzle's order: no two rows of eight in one bank
+                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4));
+                            top |= ((v.x & 0x7fff7fffu) + 0x00800080u) | ((v.y & 0x7fff7fffu) + 0x00800080u) |
+                                   ((v.z & 0x7fff7fffu) + 0x00800080u) | ((v.w & 0x7fff7fffu) + 0x00800080u);
                         }
+                    const bool bad = (top & 0x80008000u) != 0;
                     const uint32_t badw = __ballot_sync(0xffffffffu, bad);
                     if (lane == 0) S.bad[w][tile & 1][quad] = badw;   // the other parity may still be read
                     // all have looked before anyone zeroes
                     if (both) named_barrier(1, 256); else named_barrier(2 + w, 128);
                     if (w == 0 && (bad || k0 + row >= len))
-#pragma unroll
+#pragma unroll 4
                         for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -698,7 +593,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 tmem_fence_after_sync();
                 if (j == U.nk - 1) {   // the queries have been read for the last time: the next unit's, meanwhile
                     more = W.next(a);
-                    rows = more ? W.rows(a, w) : 0;
+                    rows = more ? rows_of(W, w) : 0;
                     copy_q(W, rows);
                 }
                 if (live) {
@@ -815,95 +710,6 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
     }
 }
 
-// Joins the parts of the units that the ranges' ends cut: block x takes the
-// unit that range x + 1 starts inside of, unless an earlier range does too.
-// A warp holds four rows (lane: row lane % 4, components 4 (lane / 4) and on,
-// in steps of 32), and four warps share the parts of the same rows, so that
-// few parts take one round of loads; their sums meet in shared memory, always
-// in the same order.
-constexpr int kJoinRows = 8, kJoinSplit = 4, kJoinWarps = kJoinRows / 4 * kJoinSplit;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionArgs a, int grid, int unit_rows) {
-    constexpr int kSteps = D / 32;
-    __shared__ float4 so[kJoinWarps][kSteps][32];
-    __shared__ float sl[kJoinWarps][32];
-    grid_dependency_wait();
-    const long long total = *a.total;
-    const int ranges = (int)min((long long)grid, total);
-    const int c = blockIdx.x + 1;
-    if (c >= ranges) return;
-    const RangeStart rec = a.plan[c];
-    const Line line(total, ranges);
-    auto start = [&](int x) { return line.start(x); };
-    const long long at = start(c), u0 = at - rec.kt, u1 = u0 + rec.nkt;   // the unit's stretch of the line
-    if (rec.kt == 0 || start(c - 1) > u0) return;
-    const int group = a.group;
-    const int nrows = min(unit_rows, rec.n * group - rec.rt * unit_rows);
-    if ((int)blockIdx.y * kJoinRows >= nrows) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = warp % kJoinSplit;
-    const int row = blockIdx.y * kJoinRows + warp / kJoinSplit * 4 + (lane & 3), ch = lane >> 2;
-    const bool valid = row < nrows;
-    const int first = c - 1, last = line.range_of(u1 - 1);    // ranges with a part
-    const int slot0 = 2 * first + (start(first) >= u0 ? 0 : 1);
-    auto slot = [&](int x) { return (size_t)(x == first ? slot0 : 2 * x) * a.rows; };
-    float mx = -INFINITY;
-    if (valid)
-        for (int x = first + ch; x <= last; x += 8) mx = fmaxf(mx, a.ml[slot(x) + row].x);
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    float4 o[kSteps];
-    float l = 0.f;
-#pragma unroll
-    for (int y = 0; y < kSteps; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (valid) {
-#pragma unroll 4
-        for (int x = first + split; x <= last; x += kJoinSplit) {
-            const size_t sx = slot(x);
-            const float2 ml = a.ml[sx + row];
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mx);
-            l = fmaf(f, ml.y, l);
-            const float4* src = reinterpret_cast<const float4*>(a.o) + (sx + (row & ~31)) * (D / 4) + ch * 32 + (row & 31);
-#pragma unroll
-            for (int y = 0; y < kSteps; ++y) {
-                const float4 v = src[y * 256];
-                o[y].x = fmaf(f, v.x, o[y].x);
-                o[y].y = fmaf(f, v.y, o[y].y);
-                o[y].z = fmaf(f, v.z, o[y].z);
-                o[y].w = fmaf(f, v.w, o[y].w);
-            }
-        }
-    }
-#pragma unroll
-    for (int y = 0; y < kSteps; ++y) so[warp][y][lane] = o[y];
-    sl[warp][lane] = l;
-    __syncthreads();
-    if (split != 0 || !valid) return;
-#pragma unroll
-    for (int k = 1; k < kJoinSplit; ++k) {
-        l += sl[warp + k][lane];
-#pragma unroll
-        for (int y = 0; y < kSteps; ++y) {
-            const float4 v = so[warp + k][y][lane];
-            o[y].x += v.x;
-            o[y].y += v.y;
-            o[y].z += v.z;
-            o[y].w += v.w;
-        }
-    }
-    const int gr = rec.rt * unit_rows + row;
-    const size_t orow = (size_t)(rec.t0 + gr / group) * a.heads + rec.h * group + gr % group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int y = 0; y < kSteps; ++y) {
-        const __nv_bfloat162 p0 = __floats2bfloat162_rn(o[y].x * inv, o[y].y * inv);
-        const __nv_bfloat162 p1 = __floats2bfloat162_rn(o[y].z * inv, o[y].w * inv);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + y * 32 + ch * 4) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
-    }
-    if (a.lse && ch == 0) a.lse[orow] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
-}
-
 // The cache seen as 8-row groups of swizzle atoms: {64 components, 8 rows,
 // blocks of 64, groups}; one box is a page's rows of one key head (or 128).
 bool encode_cache(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 enc, const void* base, int D, long long rows, int box_rows) {
@@ -947,22 +753,15 @@ cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtens
     cfg.gridDim = dim3(grid - 1, (rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, a, grid, (int)C::kRows);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16, D / 32, kUnitCost>, a, (int)C::kRows);
 }
 
 }  // namespace
 
-bool attention_tc_supported(const AttentionArgs& a, int dtype) {
-    if (dtype != MOE_DTYPE_BF16 || (a.D != 64 && a.D != 128)) return false;
-    // whole swizzle atoms, and pages that a tile of keys holds whole or lies inside of
-    if (a.page_size % 8 != 0 || (kKeys % a.page_size != 0 && a.page_size % kKeys != 0)) return false;
-    return a.n_pages > 0 && (long long)a.n_pages * a.kv_heads * a.page_size / 8 < 0x7fffffffLL;
-}
-
 cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s) {
     const auto enc = tensor_map_encoder();
     if (!enc || sms <= 0) return cudaErrorNotSupported;
-    const int grid = sms < kAttentionRanges ? sms : kAttentionRanges;
+    const int grid = sms < kTcRanges ? sms : kTcRanges;
     const long long rows = (long long)a.n_pages * a.kv_heads * a.page_size;
     CUtensorMap mk, mv;
     const int box = a.page_size < kKeys ? a.page_size : kKeys;

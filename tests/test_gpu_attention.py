@@ -252,7 +252,7 @@ def test_bad_tables_and_lengths_raise_the_flag_and_spare_the_others(dtype, page)
         if bad == "page":
             c.table[1, 2] = c.k.shape[0]
         elif bad == "negative page":
-            c.table[1, 0] = -7
+            c.table[1, 0] = -1
         elif bad == "length":
             c.ctx[1] = c.table.shape[1] * page - 2
         else:
