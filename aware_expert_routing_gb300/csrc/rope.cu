@@ -41,55 +41,216 @@ __global__ void rope_table_kernel(RopeArgs a) {
 }
 
 // ---- append -------------------------------------------------------------------
-// One block per token, one thread per pair or component.
-template <typename T>
-__global__ void append_kernel(AppendArgs a) {
-    const int t = blockIdx.x;
-    const int half = a.rot / 2, D = a.D;
-    const int units = half + (D - a.rot);   // pairs, then components that are not rotated
-    const float* ang = nullptr;
+// Bounded by the bytes: queries, keys and values are read once and written once.
+
+struct Place {
+    const float* angle;     // the position's cosines, then sines
+    bool keep;              // the token's key and value are written
+    long long page;
+    int row;                // of the page
+};
+
+__device__ __forceinline__ Place place_of(const AppendArgs& a, int t, bool report) {
+    Place p{};
     if (a.rot > 0) {
         int m = a.positions[t];
         if (m < 0 || m >= a.n_pos) {
-            if (threadIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
+            if (report) raise_flag(a.flags, kFlagBadIndex);
             m = m < 0 ? 0 : a.n_pos - 1;
         }
-        ang = a.rope + (size_t)m * a.rot;
+        p.angle = a.rope + (size_t)m * a.rot;
     }
     const long long slot = a.slots[t];
-    const bool keep = slot >= 0 && slot < a.n_slots;
-    if (slot >= a.n_slots && threadIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
-    const long long page = keep ? slot / a.page_size : 0;
-    const int row = keep ? (int)(slot - page * a.page_size) : 0;
-    const int nq = a.q ? a.heads : 0;
-    for (int u = threadIdx.x; u < (nq + a.kv_heads) * units; u += blockDim.x) {
+    if (slot >= a.n_slots && report) raise_flag(a.flags, kFlagBadIndex);
+    p.keep = slot >= 0 && slot < a.n_slots;
+    if (p.keep) {   // slots past 2^32 are rare: the 64-bit division is skipped
+        p.page = slot >> 32 ? slot / a.page_size : (long long)((uint32_t)slot / (uint32_t)a.page_size);
+        p.row = (int)(slot - p.page * a.page_size);
+    }
+    return p;
+}
+
+// Sixteen bytes of a row as floats, and back.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ void get(const uint4& u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ void get(const uint4& u, float (&x)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Rotations that fall on whole 16-byte words.  A block has one token (and, in
+// y, some of its rows: query heads, key heads, value heads); threadIdx.x is
+// the place in a row: a word of each half of the rotated part (half layout),
+// or a word.  It keeps its cosines and sines for all rows it goes through.
+template <typename T, bool kPairs>
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+    constexpr int N = Vec<T>::kN;
+    const int t = blockIdx.x, x = threadIdx.x, nx = blockDim.x, D = a.D;
+    const int half = a.rot / 2;
+    // half layout: words of one half, then words that are not rotated
+    const int turned = kPairs ? a.rot / N : half / N;
+    const bool turn = x < turned;
+    // the thread's word of a rotated row and its partner, and its words of a value
+    const int at = kPairs || turn ? x * N : a.rot + (x - turned) * N, at2 = !kPairs && turn ? at + half : -1;
+    const int vat = x * N, vat2 = !kPairs && (x + nx) * N < D ? (x + nx) * N : -1;
+    const int rows = a.heads + 2 * a.kv_heads, step = blockDim.y * gridDim.y;
+    grid_launch_dependents();
+    grid_dependency_wait();
+
+    // Two rows at a time; the first two are on their way before the token's
+    // place and angles are read (two loads one after the other).
+    constexpr int kAt = 2;
+    uint4 u[kAt], w[kAt];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+            const int r = r0 + i * step;
+            if (r >= rows) continue;
+            const bool is_q = r < a.heads, is_v = r >= a.heads + a.kv_heads;
+            const int kh = r - a.heads - (is_v ? a.kv_heads : 0);
+            const T* src = is_q   ? static_cast<const T*>(a.q) + t * a.q_tok + r * a.q_head
+                           : is_v ? static_cast<const T*>(a.v) + t * a.v_tok + kh * a.v_head
+                                  : static_cast<const T*>(a.k) + t * a.k_tok + kh * a.k_head;
+            u[i] = *reinterpret_cast<const uint4*>(src + (is_v ? vat : at));
+            if ((is_v ? vat2 : at2) >= 0) w[i] = *reinterpret_cast<const uint4*>(src + (is_v ? vat2 : at2));
+        }
+    };
+    int r0 = blockIdx.y * blockDim.y + threadIdx.y;
+    fetch(r0);
+    const Place p = place_of(a, t, x == 0 && threadIdx.y == 0 && blockIdx.y == 0);
+    float cs[N], sn[N];
+    if (turn) {
+        constexpr int M = kPairs ? N / 2 : N;
+        const float* c0 = p.angle + x * M;
+#pragma unroll
+        for (int i = 0; i < M; i += 2) {
+            const float2 c = *reinterpret_cast<const float2*>(c0 + i), s = *reinterpret_cast<const float2*>(c0 + half + i);
+            cs[i] = c.x; cs[i + 1] = c.y;
+            sn[i] = s.x; sn[i + 1] = s.y;
+        }
+    }
+    const long long page_at = p.page * a.kv_heads;
+    for (; r0 < rows; r0 += kAt * step) {
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+            const int r = r0 + i * step;
+            if (r >= rows) continue;
+            const bool is_q = r < a.heads, is_v = r >= a.heads + a.kv_heads;
+            const int kh = r - a.heads - (is_v ? a.kv_heads : 0);
+            if (!is_q && !p.keep) continue;
+            T* dst = is_q ? static_cast<T*>(a.q_out) + t * a.out_tok + r * a.out_head
+                          : static_cast<T*>(is_v ? a.cv : a.ck) + ((page_at + kh) * a.page_size + p.row) * D;
+            uint4 y = u[i], z = w[i];
+            if (turn && !is_v) {
+                float v[N], b[N], o[N], o2[N];
+                Vec<T>::get(u[i], v);
+                if (kPairs) {
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        o[e] = v[e] * cs[e / 2] - v[e + 1] * sn[e / 2];
+                        o[e + 1] = v[e + 1] * cs[e / 2] + v[e] * sn[e / 2];
+                    }
+                } else {
+                    Vec<T>::get(w[i], b);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        o[e] = v[e] * cs[e] - b[e] * sn[e];
+                        o2[e] = b[e] * cs[e] + v[e] * sn[e];
+                    }
+                    z = Vec<T>::put(o2);
+                }
+                y = Vec<T>::put(o);
+            }
+            *reinterpret_cast<uint4*>(dst + (is_v ? vat : at)) = y;
+            if ((is_v ? vat2 : at2) >= 0) *reinterpret_cast<uint4*>(dst + (is_v ? vat2 : at2)) = z;
+        }
+        if (r0 + kAt * step < rows) fetch(r0 + kAt * step);
+    }
+}
+
+// Any even rotation: one thread per pair or component.
+template <typename T>
+__global__ void append_any_kernel(const AppendArgs a) {
+    const int t = blockIdx.x;
+    const int half = a.rot / 2, D = a.D;
+    const int units = half + (D - a.rot);   // pairs, then components that are not rotated
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const Place p = place_of(a, t, threadIdx.x == 0);
+    for (int u = threadIdx.x; u < (a.heads + a.kv_heads) * units; u += blockDim.x) {
         const int h = u / units, c = u - h * units;
-        const bool is_q = h < nq;
-        const int kh = h - nq;
+        const bool is_q = h < a.heads;
+        const int kh = h - a.heads;
+        if (!is_q && !p.keep) continue;
         const T* src = is_q ? (const T*)a.q + t * a.q_tok + h * a.q_head : (const T*)a.k + t * a.k_tok + kh * a.k_head;
         T* dst = is_q ? (T*)a.q_out + t * a.out_tok + h * a.out_head
-                      : (T*)a.ck + ((page * a.kv_heads + kh) * a.page_size + row) * D;
-        if (!is_q && !keep) continue;
+                      : (T*)a.ck + ((p.page * a.kv_heads + kh) * a.page_size + p.row) * D;
         if (c < half) {
             const int i0 = a.interleaved ? 2 * c : c, i1 = a.interleaved ? 2 * c + 1 : c + half;
-            const float x = to_float(src[i0]), y = to_float(src[i1]), cs = ang[c], sn = ang[half + c];
+            const float x = to_float(src[i0]), y = to_float(src[i1]), cs = p.angle[c], sn = p.angle[half + c];
             dst[i0] = from_float<T>(x * cs - y * sn);
             dst[i1] = from_float<T>(y * cs + x * sn);
         } else {
             dst[c + half] = src[c + half];
         }
     }
-    if (!keep) return;
+    if (!p.keep) return;
     for (int u = threadIdx.x; u < a.kv_heads * D; u += blockDim.x) {
         const int h = u / D, c = u - h * D;
-        ((T*)a.cv)[((page * a.kv_heads + h) * a.page_size + row) * D + c] = ((const T*)a.v)[t * a.v_tok + h * a.v_head + c];
+        ((T*)a.cv)[((p.page * a.kv_heads + h) * a.page_size + p.row) * D + c] = ((const T*)a.v)[t * a.v_tok + h * a.v_head + c];
     }
 }
 
-cudaError_t launch_append(const AppendArgs& a, int dtype, cudaStream_t s) {
-    if (dtype == MOE_DTYPE_BF16) append_kernel<__nv_bfloat16><<<a.T, 256, 0, s>>>(a);
-    else append_kernel<float><<<a.T, 256, 0, s>>>(a);
-    return cudaGetLastError();
+template <typename T>
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+    constexpr int N = Vec<T>::kN;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // whole words: a half of the rotated part (half layout), or all of it
+    if (a.interleaved ? a.rot % N != 0 : a.rot / 2 % N != 0) {
+        cfg.gridDim = dim3(a.T);
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, append_any_kernel<T>, a);
+    }
+    const bool pairs = a.interleaved || a.rot == 0;
+    const int nx = pairs ? a.D / N : a.rot / 2 / N + (a.D - a.rot) / N;
+    const int rows = a.heads + 2 * a.kv_heads;
+    // Few tokens: a row per thread, spread over blocks.  Many: each thread
+    // goes through several rows with the same cosines and sines.
+    const int most = 256 / nx, each = (rows + most - 1) / most;
+    const int ny = (rows + each - 1) / each;
+    cfg.gridDim = dim3(a.T, a.T <= 304 ? each : 1);
+    cfg.blockDim = dim3(nx, ny);
+    return pairs ? cudaLaunchKernelEx(&cfg, append_kernel<T, true>, a) : cudaLaunchKernelEx(&cfg, append_kernel<T, false>, a);
 }
 
 }  // namespace
@@ -186,7 +347,8 @@ moe_status moe_kv_append(const void* q, const void* k, const void* v, const floa
     a.n_slots = (long long)cache->n_pages * cache->page_size;
     a.q_tok = p->q_tok; a.q_head = p->q_head; a.k_tok = p->k_tok; a.k_head = p->k_head;
     a.v_tok = p->v_tok; a.v_head = p->v_head; a.out_tok = p->out_tok; a.out_head = p->out_head;
-    const cudaError_t e = launch_append(a, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache->dtype == MOE_DTYPE_BF16 ? launch_append<__nv_bfloat16>(a, s) : launch_append<float>(a, s);
     return e == cudaSuccess ? MOE_OK : report(MOE_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
 }
 
