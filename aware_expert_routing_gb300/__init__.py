@@ -3,7 +3,10 @@
 Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  PyTorch supplies device memory (tensors) and streams; the
 functions below take torch tensors, check dtypes/devices, and pass raw
-pointers to the C ABI declared in include/moe.h under the same names.
+pointers to the C ABI declared in include/moe.h under the same names.  The
+calls that run several times a token (moe_kv_append, moe_tree_attention,
+moe_route_scores) do their checking and passing in an extension module
+(csrc/binding.cpp), in a few microseconds less.
 
 There is no fallback: if the shared library is missing or fails to load,
 importing the functions raises.
@@ -12,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib
 import os
 
 import torch
@@ -179,6 +183,17 @@ def load(path: str | None = None):
     if path is None:
         _lib = lib
     return lib
+
+
+_fast = None
+
+
+def _load_binding():
+    """The extension module over the same library.  Raises if it is missing."""
+    global _fast
+    load()
+    _fast = importlib.import_module("._binding", __name__)
+    return _fast
 
 
 @dataclasses.dataclass
@@ -522,13 +537,9 @@ class SelectParams:
 def moe_route_scores(scores, select_bias, params: RouteParams, select: SelectParams, routing: Routing,
                      workspace: torch.Tensor, stream=None):
     """Selection and grouping of given router scores ([B][N] fp32)."""
-    _need(scores, torch.float32, "scores")
-    if scores.shape != (params.B, params.N):
-        raise ValueError(f"scores must be [{params.B}][{params.N}]")
-    _need_bias(select_bias, params.N)
-    st = load().moe_route_scores(_ptr(scores), _ptr(select_bias), ctypes.byref(params.c()), ctypes.byref(select.c()),
-                                 ctypes.byref(routing.c()), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, "moe_route_scores")
+    st = (_fast or _load_binding()).route_scores(scores, select_bias, params, select, routing, workspace, stream)
+    if st:
+        _check(st, "moe_route_scores")
     return routing
 
 
@@ -628,6 +639,7 @@ class KvCache:
         self._c = _KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr() if page_table is not None else None,
                            self.n_pages, self.page_size, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
                            DTYPE_BF16 if k.dtype == torch.bfloat16 else DTYPE_F32)
+        self._at = ctypes.addressof(self._c)
 
     def c(self) -> _KvCache:
         return self._c
@@ -646,47 +658,15 @@ def alloc_attention_workspace(T: int, heads: int, cache: KvCache, device) -> tor
     return torch.zeros(moe_attention_workspace_bytes(T, heads, cache), dtype=torch.uint8, device=device)
 
 
-def _need_heads(t, dtype, shape, name):
-    """A CUDA tensor [tokens][heads][head_dim] whose heads are dense inside."""
-    if t.dtype != dtype or not t.is_cuda or t.shape != shape:
-        raise ValueError(f"{name} must be a CUDA tensor {tuple(shape)} of {dtype}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}: the components of a head must be adjacent")
-    return s
-
-
 def moe_kv_append(q, k, v, rope, positions, slots, cache: KvCache, q_out, workspace: torch.Tensor,
                   interleaved: bool = False, stream=None):
     """Rotates q (into q_out) and k, and writes k and v into the cache.
     q and k/v: [T][heads][head_dim] and [T][kv_heads][head_dim], any distances
     between tokens and heads that are multiples of 16 bytes; rope: the table
     of moe_rope_table, or None (no rotation); q and q_out may both be None."""
-    T, D, dt = k.shape[0], cache.head_dim, cache.dtype
-    ks = _need_heads(k, dt, (T, cache.kv_heads, D), "k")
-    vs = _need_heads(v, dt, (T, cache.kv_heads, D), "v")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out must both be given, or neither")
-    heads, qs, os_ = 0, (0, 0), (0, 0)
-    if q is not None:
-        heads = q.shape[1]
-        qs = _need_heads(q, dt, (T, heads, D), "q")
-        os_ = _need_heads(q_out, dt, (T, heads, D), "q_out")
-    n_pos, rot = 0, 0
-    if rope is not None:
-        _need(rope, torch.float32, "rope")
-        n_pos, rot = rope.shape
-        _need(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError(f"positions must hold {T} values")
-    _need(slots, torch.int64, "slots")
-    if slots.numel() != T:
-        raise ValueError(f"slots must hold {T} values")
-    prm = _Append(T, heads, rot, n_pos, int(interleaved), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    st = load().moe_kv_append(_ptr(q), _ptr(k), _ptr(v), _ptr(rope), _ptr(positions), _ptr(slots), ctypes.byref(prm),
-                              ctypes.byref(cache.c()), _ptr(q_out), _ptr(workspace), workspace.numel(),
-                              _stream(stream))
-    _check(st, "moe_kv_append")
+    st = (_fast or _load_binding()).kv_append(q, k, v, rope, positions, slots, cache._at, q_out, workspace, interleaved, stream)
+    if st:
+        _check(st, "moe_kv_append")
     return q_out
 
 
@@ -712,34 +692,9 @@ def moe_tree_attention(q, q_offsets, ctx_len, mask, cache: KvCache, out, lse, wo
     ctx_len[r] positions, and of the step's own tokens those that mask ([T]
     [words] int32 bits) allows (None: the token itself and those before it).
     scale: 1 / sqrt(head_dim) by default.  lse may be None."""
-    if q.dim() != 3:
-        raise ValueError("q must be [T][heads][head_dim]")
-    T, heads = q.shape[0], q.shape[1]
-    D, dt = cache.head_dim, cache.dtype
-    qs = _need_heads(q, dt, (T, heads, D), "q")
-    _need(out, dt, "out")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if lse.shape != (T, heads):
-            raise ValueError(f"lse must be [{T}][{heads}]")
-    R = cache.n_requests
-    _need(q_offsets, torch.int32, "q_offsets")
-    _need(ctx_len, torch.int32, "ctx_len")
-    if q_offsets.numel() != R + 1 or ctx_len.numel() != R:
-        raise ValueError(f"q_offsets must hold {R + 1} values and ctx_len {R}")
-    words = 0
-    if mask is not None:
-        _need(mask, torch.int32, "mask")
-        if mask.dim() != 2 or mask.shape[0] != T:
-            raise ValueError(f"mask must be [{T}][words]")
-        words = mask.shape[1]
-    prm = _Attention(T, heads, words, D ** -0.5 if scale is None else scale, qs[0], qs[1])
-    st = load().moe_tree_attention(_ptr(q), _ptr(q_offsets), _ptr(ctx_len), _ptr(mask), ctypes.byref(prm),
-                                   ctypes.byref(cache.c()), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                   _stream(stream))
-    _check(st, "moe_tree_attention")
+    st = (_fast or _load_binding()).tree_attention(q, q_offsets, ctx_len, mask, cache._at, out, lse, workspace, scale, stream)
+    if st:
+        _check(st, "moe_tree_attention")
     return out
 
 

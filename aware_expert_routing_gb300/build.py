@@ -1,21 +1,25 @@
 """Builds libaware_moe.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
 Each .cu file is compiled in parallel, then linked into one shared library
-next to this file.  Set MOE_PTXAS_VERBOSE=1 to print register and shared
+next to this file; binding.cpp becomes the extension module _binding.so,
+which links to it.  Set MOE_PTXAS_VERBOSE=1 to print register and shared
 memory usage per kernel.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libaware_moe.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "router.cu", "route.cu", "ffn_tc.cu", "ffn_f32.cu", "synth.cu", "pack.cu", "residency.cu",
            "static_scratch.cu", "rope.cu", "attention.cu",
@@ -29,6 +33,20 @@ def nvcc() -> str:
     return path
 
 
+def compile_binding(obj: str):
+    """binding.cpp with the host compiler, against Python's, torch's and
+    CUDA's headers."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), os.path.join(HERE, "..", "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd + [x for i in inc for x in ("-isystem", i)], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return os.path.join(torch_dir, "lib")
+
+
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(HERE, "..", "include", "moe.h"))
@@ -36,9 +54,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
 
 
@@ -61,14 +79,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    bind = os.path.join(BUILD, "binding.o")
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_lib = ex.submit(compile_binding, bind)
         objs = list(ex.map(compile_one, SOURCES))
+        torch_lib = torch_lib.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
+    cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname," + os.path.basename(LIB), "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, bind, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + torch_lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+           "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
