@@ -53,22 +53,19 @@ constexpr int kKeys = 128;     // keys per tile
 constexpr int kRowsTile = 128; // query rows per tile
 constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O from here
 constexpr int kUnitCost = 5;   // see attention_line.cuh; 2: 32.7, 3: 31.9, 4: 30.6, 6: 29.5 us for 16 trees of 16 to 4000
+constexpr int kUnroll = 1;
 constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
 
 // Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
 // (taddr >> 16) + l, from column taddr & 0xffff; complete on return.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
         "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127"
-        "}, [%128];\n"
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+        "}, [%64];\n"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
@@ -77,15 +74,7 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
           "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
           "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
           "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
-          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
-          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
-          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
-          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
-          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
-          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
-          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
-          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
         : "r"(taddr)
         : "memory");
 }
@@ -194,7 +183,7 @@ struct Cfg {
 };
 
 struct Control {
-    uint64_t full[16], empty[16], q_full[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t full[16], empty[16], q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2];
     long long wait_cycles;
     LineStart start;
     int abort_flag;
@@ -268,6 +257,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.q_full[i], 4);
             mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_half[i], 4);
             mbar_init(&S.p_full[i], 4);
             mbar_init(&S.pv_done[i], 1);
         }
@@ -293,7 +283,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         // no work for this CTA
     } else if (warp == 0) {
         // ---- producer: pages into the ring, in the order in which the MMAs read them ----
-        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         uint32_t seq = 0;
         const int page = a.page_size;
         const int per = page < kKeys ? kKeys / page : 1;        // pages of a tile
@@ -361,7 +351,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         }
     } else if (warp == 1) {
         // ---- MMA: one thread issues, in the order of the ring ----
-        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
         constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
         const uint32_t ctl = uniform(smem_u32(&S)), ring0 = uniform(smem_u32(ring)), q0 = uniform(smem_u32(qs)), tm = uniform(tmem);
@@ -395,11 +385,17 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                        k_hi | (ka + ((k / 4) * 1024 + (k % 4) * 32) / 16), idesc_s, k > 0);
             mma_commit(ctl + (uint32_t)offsetof(Control, s_full) + 8 * (buf));
         };
-        auto issue_pv = [&](int w, uint32_t buf, uint32_t vaddr, uint32_t acc) {
+        // The product with V starts with the first 64 keys' P.
+        auto issue_pv = [&](int w, uint32_t buf, uint32_t pp, uint32_t vaddr, uint32_t acc) {
             const uint32_t va = vaddr >> 4, d = tm + kOCol + w * D, p = tm + buf * 128;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
+            for (int k = 0; k < kKeys / 16; ++k) {
+                if (k == kKeys / 32) {
+                    wait_bar(&S.p_full[buf], pp, S, a.flags);
+                    tmem_fence_after_sync();
+                }
                 mma_ts(d, p + k * 8, v_hi | (va + k * 2 * C::kBlocks * 1024 / 16), idesc_o, k > 0 ? 1u : acc);
+            }
             mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
         };
         do {
@@ -421,10 +417,11 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                         advance();
                     }
                     const uint32_t buf = tile[0] & 1;
-                    wait_bar(&S.p_full[buf], (tile[0] >> 1) & 1, S, a.flags);
+                    const uint32_t pp = (tile[0] >> 1) & 1;
+                    wait_bar(&S.p_half[buf], pp, S, a.flags);
                     const uint32_t vaddr = stage_wait(st, ph);
                     if (warp_aborted(S)) break;
-                    issue_pv(0, buf, vaddr, j > 0);
+                    issue_pv(0, buf, pp, vaddr, j > 0);
                     mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                     advance();
                     ++tile[0];
@@ -444,12 +441,13 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     advance();
                     uint32_t vaddr = 0;
                     for (int w = 0; w < nw; ++w) {
-                        wait_bar(&S.p_full[w], tile[w] & 1, S, a.flags);
+                        const uint32_t pp = tile[w] & 1;
+                        wait_bar(&S.p_half[w], pp, S, a.flags);
                         ++tile[w];
                         if (w == 0) vaddr = stage_wait(v_st, v_ph);
                         tmem_fence_after_sync();
                         if (warp_aborted(S)) break;
-                        issue_pv(w, w, vaddr, j > 0);
+                        issue_pv(w, w, pp, vaddr, j > 0);
                         if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (v_st));
                         if (j + 1 < n) {
                             if (w == 0) kaddr = stage_wait(st, ph);
@@ -465,11 +463,11 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             if (warp_aborted(S)) break;
         } while (W.next(a));
     } else if (warp < C::kFirst) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     } else {
         // ---- softmax: warpgroup w owns row tile w, thread = row = TMEM lane ----
-        // registers: 384 x 168 at launch = 128 x 56 + 256 x 224
-        if (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        // registers: 384 x 168 at launch = 128 x 120 + 256 x 192
+        if (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int w = (warp - C::kFirst) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -597,16 +595,25 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     copy_q(W, rows);
                 }
                 if (live) {
-                    uint32_t s[128];
-                    tmem_ld128(lanes + buf * 128, s);
-                    if (masked) {
+                    // Two passes over S, 64 columns at a time: the maximum, then
+                    // P.  (All 128 in registers at once spill, and take longer.)
+                    uint32_t s[64];
+                    auto load_s = [&](int x) {
+                        tmem_ld64(lanes + buf * 128 + x * 64, s);
+                        if (masked) {
+                            const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
 #pragma unroll
-                        for (int x = 0; x < 128; ++x)
-                            if (!((bits[x >> 5] >> (x & 31)) & 1u)) s[x] = 0xff800000u;   // -inf
-                    }
+                            for (int y = 0; y < 64; ++y)
+                                if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) s[y] = 0xff800000u;   // -inf
+                        }
+                    };
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll kUnroll
+                    for (int x = 0; x < 2; ++x) {
+                        load_s(x);
 #pragma unroll
-                    for (int x = 0; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                        for (int y = 0; y < 64; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
+                    }
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (j == 0) {
                         m = mt;
@@ -617,7 +624,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             const float mn = fmaxf(m, mt), f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                             wait_pv(tile - 1);
                             tmem_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                             for (int x = 0; x < D / 32; ++x) {
                                 uint32_t o[32];
                                 tmem_ld32(lanes + kOCol + w * D + x * 32, o);
@@ -632,26 +639,36 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     const float off = m == -INFINITY ? 0.f : -m * c;
                     const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
                     uint64_t sum[2] = {0, 0};
+#pragma unroll kUnroll
+                    for (int x = 0; x < 2; ++x) {
+                        load_s(x);
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        float p0, p1;
-                        unpack2(fma2(pack2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, off2), p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
-                        const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
-                        s[x] = *reinterpret_cast<const uint32_t*>(&p);
+                        for (int y = 0; y < 32; ++y) {
+                            float p0, p1;
+                            unpack2(fma2(pack2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, off2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+                            s[y] = *reinterpret_cast<const uint32_t*>(&p);
+                        }
+                        tmem_st32(lanes + buf * 128 + x * 32, s);   // over columns of S that have been read
+                        tmem_wait_st();
+                        tmem_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(x ? &S.p_full[buf] : &S.p_half[buf]);
                     }
                     float s0, s1;
                     unpack2(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1 + poison;
-                    tmem_st32(lanes + buf * 128, s);
-                    tmem_st32(lanes + buf * 128 + 32, s + 32);
-                    tmem_wait_st();
+                } else {
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&S.p_half[buf]);
+                        mbar_arrive(&S.p_full[buf]);
+                    }
                 }
-                tmem_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.p_full[buf]);
                 ++tile;
             }
             seq += 2 * U.nk;
@@ -664,8 +681,8 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 // 32 rows of a part lie side by side: [D / 4][32] float4
                 float4* part = reinterpret_cast<float4*>(a.o) + ((size_t)slot * a.rows + w * kRowsTile + quad * 32) * (D / 4) + lane;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {   // (rolled: this code runs once or twice, its fetch counts)
                     uint32_t o[32];
                     __syncwarp();   // the load is the whole warp's
                     tmem_ld32(lanes + kOCol + w * D + x * 32, o);
