@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const float c = a.scale * 1.4426950408889634f;   // scores to powers of two
 
+    prefetch_tables(a);
     grid_launch_dependents();
     grid_dependency_wait();
     find_start<kRows, kKeys, kPlainCost, 256>(a, S);
@@ -276,11 +277,7 @@ cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, attention_plain_kernel<T, kC, kR>, a)) != cudaSuccess) return e;
     if ((long long)a.max_pages * a.page_size <= P::kKeys || grid < 2) return cudaSuccess;   // no unit is cut
-    const int rows = a.rows < P::kRows ? a.rows : P::kRows;
-    cfg.gridDim = dim3(grid - 1, (rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, 2 * kC, kPlainCost>, a, (int)P::kRows);
+    return launch_join<T, 2 * kC, kPlainCost>(a, grid, P::kRows, cfg);
 }
 
 template <typename T>

@@ -111,6 +111,24 @@ struct LineWalk {
     __device__ __forceinline__ int rows(const AttentionArgs& a) const { return min(kRows, q.n * a.group - rt * kRows); }
 };
 
+// Brings the lengths and the page table towards L2, each CTA a part of them,
+// while the kernel before this one ends: they are read one after the other
+// once it has.  (A prefetch reads nothing that can go stale: L2 is where the
+// other kernel's writes go.)
+__device__ __forceinline__ void prefetch_tables(const AttentionArgs& a) {
+    const int lane = threadIdx.x & 31;
+    auto line = [](const void* p, long long bytes, long long l) {
+        if (l * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + l * 128));
+    };
+    if (threadIdx.x < 32) {
+        line(a.page_table, (long long)a.R * a.max_pages * 4, (long long)blockIdx.x * 32 + lane);
+        if (blockIdx.x == 0) {
+            line(a.q_offsets, (a.R + 1) * 4LL, lane);
+            line(a.ctx_len, a.R * 4LL, lane);
+        }
+    }
+}
+
 // Finds this CTA's range.  All kThreads threads; each adds up a few consecutive
 // requests, and the one whose requests hold the range's start writes it down.
 // The caller synchronises before S is read.
@@ -199,14 +217,17 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, float4 o, float l)
 // Joins the parts of the units that the ranges' ends cut: block x takes the
 // unit that range x + 1 starts inside of, unless an earlier range does too.
 // A warp holds four rows (lane: row lane % 4, components 4 (lane / 4) and on,
-// in steps of 32), and four warps share the parts of the same rows, so that
-// few parts take one round of loads; their sums meet in shared memory, always
-// in the same order.  (16 rows a block: 35.1 against 32.7 us for 16 trees of 16
-// to 4000, fewer of the larger blocks are resident.)  kSteps: ceil(D / 32).
-constexpr int kJoinRows = 8, kJoinSplit = 4, kJoinWarps = kJoinRows / 4 * kJoinSplit;
+// in steps of 32), and kJoinSplit warps share the parts of the same rows, so
+// that few parts take one round of loads; their sums meet in shared memory,
+// always in the same order.  Eight warps a block: all on four rows for units of
+// few rows, where latency counts, else four on each four of eight.  (16 rows a
+// block: 35.1 against 32.7 us for 16 trees of 16 to 4000, fewer of the larger
+// blocks are resident.)  kSteps: ceil(D / 32).
+constexpr int kJoinWarps = 8;
 
-template <typename T, int kSteps, int kUnitCost>
+template <typename T, int kSteps, int kUnitCost, int kJoinSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionArgs a, int unit_rows) {
+    constexpr int kJoinRows = 4 * kJoinWarps / kJoinSplit;
     const int D = a.D;
     __shared__ float4 so[kJoinWarps][kSteps][32];
     __shared__ float sl[kJoinWarps][32];
@@ -286,6 +307,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     for (int y = 0; y < kSteps; ++y)
         if (y * 8 + ch < D / 4) store_row(static_cast<T*>(a.out) + orow * D + y * 32 + ch * 4, o[y], l);
     if (a.lse && ch == 0) a.lse[orow] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+}
+
+// Launches the join for a kernel of `ranges` ranges and units of up to
+// unit_rows rows (cfg: stream and attributes).
+template <typename T, int kSteps, int kUnitCost>
+cudaError_t launch_join(const AttentionArgs& a, int ranges, int unit_rows, cudaLaunchConfig_t cfg) {
+    const int rows = a.rows < unit_rows ? a.rows : unit_rows;
+    const bool few = rows <= 32;
+    cfg.gridDim = dim3(ranges - 1, (rows + (few ? 3 : 7)) / (few ? 4 : 8));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return few ? cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kSteps, kUnitCost, 8>, a, unit_rows)
+               : cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kSteps, kUnitCost, 4>, a, unit_rows);
 }
 
 }  // namespace

@@ -268,6 +268,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         prefetch_tensormap(&map_v);
     }
     if (warp == 1) tmem_alloc(&S.tmem_base, 512);
+    prefetch_tables(a);
     grid_launch_dependents();   // a kernel that follows may start its prologue; it waits for this grid's end
     grid_dependency_wait();     // lengths, queries and the cache come from preceding kernels
 
@@ -766,11 +767,7 @@ cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtens
     if (e != cudaSuccess) return e;
     // a unit of one key tile is never cut
     if ((long long)a.max_pages * a.page_size <= kKeys || grid < 2) return cudaSuccess;
-    const int rows = a.rows < C::kRows ? a.rows : C::kRows;
-    cfg.gridDim = dim3(grid - 1, (rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16, D / 32, kUnitCost>, a, (int)C::kRows);
+    return launch_join<__nv_bfloat16, D / 32, kUnitCost>(a, grid, C::kRows, cfg);
 }
 
 }  // namespace
