@@ -399,20 +399,20 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             }
             mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
         };
+        // Once a wait has given up, all return at once: the loop then runs out on
+        // whatever the shared and tensor memory hold, which harms nothing.
         do {
             const int nw = uniform(kTiles == 2 && rows_of(W, 1) > 0 ? 2 : 1);
             const int n = uniform(W.nk);
             if (kTiles == 1) {
                 wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
                 uint32_t kaddr = stage_wait(st, ph);
-                if (warp_aborted(S)) break;
                 issue_s(0, tile[0] & 1, kaddr);
                 mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                 advance();
                 for (int j = 0; j < n; ++j) {
                     if (j + 1 < n) {
                         kaddr = stage_wait(st, ph);
-                        if (warp_aborted(S)) break;
                         issue_s(0, (tile[0] + 1) & 1, kaddr);
                         mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                         advance();
@@ -421,7 +421,6 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     const uint32_t pp = (tile[0] >> 1) & 1;
                     wait_bar(&S.p_half[buf], pp, S, a.flags);
                     const uint32_t vaddr = stage_wait(st, ph);
-                    if (warp_aborted(S)) break;
                     issue_pv(0, buf, pp, vaddr, j > 0);
                     mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                     advance();
@@ -431,10 +430,8 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 uint32_t kaddr = stage_wait(st, ph);
                 for (int w = 0; w < nw; ++w) {
                     wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
-                    if (warp_aborted(S)) break;
                     issue_s(w, w, kaddr);
                 }
-                if (warp_aborted(S)) break;
                 mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                 advance();
                 for (int j = 0; j < n; ++j) {
@@ -447,21 +444,17 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                         ++tile[w];
                         if (w == 0) vaddr = stage_wait(v_st, v_ph);
                         tmem_fence_after_sync();
-                        if (warp_aborted(S)) break;
                         issue_pv(w, w, pp, vaddr, j > 0);
                         if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (v_st));
                         if (j + 1 < n) {
                             if (w == 0) kaddr = stage_wait(st, ph);
-                            if (warp_aborted(S)) break;
                             issue_s(w, w, kaddr);
                             if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                         }
                     }
-                    if (warp_aborted(S)) break;
                     if (j + 1 < n) advance();
                 }
             }
-            if (warp_aborted(S)) break;
         } while (W.next(a));
     } else if (warp < C::kFirst) {
         if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
