@@ -53,7 +53,6 @@ constexpr int kKeys = 128;     // keys per tile
 constexpr int kRowsTile = 128; // query rows per tile
 constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O from here
 constexpr int kUnitCost = 5;   // see attention_line.cuh; 2: 32.7, 3: 31.9, 4: 30.6, 6: 29.5 us for 16 trees of 16 to 4000
-constexpr int kUnroll = 1;
 constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
 
 // Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
@@ -589,24 +588,30 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     copy_q(W, rows);
                 }
                 if (live) {
-                    // Two passes over S, 64 columns at a time: the maximum, then
-                    // P.  (All 128 in registers at once spill, and take longer.)
-                    uint32_t s[64];
+                    // The maximum, then P, 64 columns at a time.  With one row
+                    // tile the row stays in registers between the two; with two
+                    // (192 registers) it would spill, and S is read twice: 117
+                    // against 121 us for 1x64 at 131000.  (One tile: 27.6
+                    // against 28.4 us for 16 trees of 16 to 4000.)
+                    constexpr bool kHold = kTiles == 1;
+                    constexpr int kTimes = kHold ? 2 : 1;
+                    uint32_t s[kTimes][64];
                     auto load_s = [&](int x) {
-                        tmem_ld64(lanes + buf * 128 + x * 64, s);
+                        uint32_t(&h)[64] = s[kHold ? x : 0];
+                        tmem_ld64(lanes + buf * 128 + x * 64, h);
                         if (masked) {
                             const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
 #pragma unroll
                             for (int y = 0; y < 64; ++y)
-                                if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) s[y] = 0xff800000u;   // -inf
+                                if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) h[y] = 0xff800000u;   // -inf
                         }
                     };
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll kUnroll
+#pragma unroll kTimes
                     for (int x = 0; x < 2; ++x) {
                         load_s(x);
 #pragma unroll
-                        for (int y = 0; y < 64; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[y]));
+                        for (int y = 0; y < 64; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[kHold ? x : 0][y]));
                     }
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if (j == 0) {
@@ -633,20 +638,21 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     const float off = m == -INFINITY ? 0.f : -m * c;
                     const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
                     uint64_t sum[2] = {0, 0};
-#pragma unroll kUnroll
+#pragma unroll kTimes
                     for (int x = 0; x < 2; ++x) {
-                        load_s(x);
+                        if (!kHold) load_s(x);
+                        uint32_t(&h)[64] = s[kHold ? x : 0];
 #pragma unroll
                         for (int y = 0; y < 32; ++y) {
                             float p0, p1;
-                            unpack2(fma2(pack2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, off2), p0, p1);
+                            unpack2(fma2(pack2(__uint_as_float(h[2 * y]), __uint_as_float(h[2 * y + 1])), c2, off2), p0, p1);
                             p0 = ex2(p0);
                             p1 = ex2(p1);
                             sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
                             const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
-                            s[y] = *reinterpret_cast<const uint32_t*>(&p);
+                            h[y] = *reinterpret_cast<const uint32_t*>(&p);
                         }
-                        tmem_st32(lanes + buf * 128 + x * 32, s);   // over columns of S that have been read
+                        tmem_st32(lanes + buf * 128 + x * 32, h);   // over columns of S that have been read
                         tmem_wait_st();
                         tmem_fence_before_sync();
                         __syncwarp();
