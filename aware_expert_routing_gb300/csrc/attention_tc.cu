@@ -513,9 +513,21 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             if (lane == 0) mbar_arrive(&S.q_full[w]);
         };
 
+        // The mask words of this row's token in a unit, on their way early.
+        uint32_t mw[2];
+        auto read_mask = [&](const Walk& U, int rows) {
+            mw[0] = mw[1] = 0u;
+            if (!a.mask || row >= rows) return;
+            const int gr = U.rt * C::kRows + w * kRowsTile + row;
+            const uint32_t* mrow = a.mask + (size_t)(U.q.t0 + gr / group) * a.mask_words;
+            mw[0] = mrow[0];
+            if (a.mask_words > 1) mw[1] = mrow[1];
+        };
+
         int rows = rows_of(W, w);
         if (rows > 0) {
             copy_q(W, rows);
+            read_mask(W, rows);
             finish_q();
         }
         bool more = true;
@@ -530,6 +542,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 rows = more ? rows_of(W, w) : 0;
                 if (rows > 0) {
                     copy_q(W, rows);
+                    read_mask(W, rows);
                     finish_q();
                 }
                 continue;
@@ -542,7 +555,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             const size_t orow = (size_t)(U.q.t0 + ti) * a.heads + U.h * group + (gr - ti * group);
             const bool whole = U.nk == U.q.nkt;
             const int slot = 2 * blockIdx.x + (U.first ? 0 : 1);
-            const uint32_t mw0 = mrow && a.mask_words > 0 ? mrow[0] : 0u, mw1 = mrow && a.mask_words > 1 ? mrow[1] : 0u;
+            const uint32_t mw0 = mw[0], mw1 = mw[1];
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < U.nk; ++j) {
                 const uint32_t buf = kTiles == 1 ? (tile & 1) : (uint32_t)w;
@@ -551,61 +564,35 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 const bool masked = k0 + kKeys > U.q.ctx;
                 uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
                 float poison = 0.f;
-                if (masked) {
-                    seen_bits(mrow, a.mask_words, mw0, mw1, ti, n, k0 - U.q.ctx, bits);
-                    // value rows past the context: zero those past the length, and those that are not finite
-                    const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
-                    wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
-                    unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (row >> 3) * (C::kBlocks * 1024) + (row & 7) * 128;
-                    // (a bf16 of all-ones exponent carries into bit 15 when 0x80 is added)
-                    uint32_t top = 0;
-                    if (k0 + row >= U.q.ctx && k0 + row < len)
-#pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x) {   // the swizzle's order: no two rows of eight in one bank
-                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4));
-                            top |= ((v.x & 0x7fff7fffu) + 0x00800080u) | ((v.y & 0x7fff7fffu) + 0x00800080u) |
-                                   ((v.z & 0x7fff7fffu) + 0x00800080u) | ((v.w & 0x7fff7fffu) + 0x00800080u);
-                        }
-                    const bool bad = (top & 0x80008000u) != 0;
-                    const uint32_t badw = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0) S.bad[w][tile & 1][quad] = badw;   // the other parity may still be read
-                    // all have looked before anyone zeroes
-                    if (both) named_barrier(1, 256); else named_barrier(2 + w, 128);
-                    if (w == 0 && (bad || k0 + row >= len))
-#pragma unroll 4
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (bits[x] & S.bad[w][tile & 1][x]) poison = NAN;
-                }
+                if (masked) seen_bits(mrow, a.mask_words, mw0, mw1, ti, n, k0 - U.q.ctx, bits);
                 wait_bar(&S.s_full[buf], sph, S, a.flags);
                 tmem_fence_after_sync();
                 if (j == U.nk - 1) {   // the queries have been read for the last time: the next unit's, meanwhile
                     more = W.next(a);
                     rows = more ? rows_of(W, w) : 0;
                     copy_q(W, rows);
+                    read_mask(W, rows);
                 }
-                if (live) {
-                    // The maximum, then P, 64 columns at a time.  With one row
-                    // tile the row stays in registers between the two; with two
-                    // (192 registers) it would spill, and S is read twice: 117
-                    // against 121 us for 1x64 at 131000.  (One tile: 27.6
-                    // against 28.4 us for 16 trees of 16 to 4000.)
-                    constexpr bool kHold = kTiles == 1;
-                    constexpr int kTimes = kHold ? 2 : 1;
-                    uint32_t s[kTimes][64];
-                    auto load_s = [&](int x) {
-                        uint32_t(&h)[64] = s[kHold ? x : 0];
-                        tmem_ld64(lanes + buf * 128 + x * 64, h);
-                        if (masked) {
-                            const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
+                // The maximum, then P, 64 columns at a time.  With one row
+                // tile the row stays in registers between the two; with two
+                // (192 registers) it would spill, and S is read twice: 117
+                // against 121 us for 1x64 at 131000.  (One tile: 27.6
+                // against 28.4 us for 16 trees of 16 to 4000.)
+                constexpr bool kHold = kTiles == 1;
+                constexpr int kTimes = kHold ? 2 : 1;
+                uint32_t s[kTimes][64];
+                auto load_s = [&](int x) {
+                    uint32_t(&h)[64] = s[kHold ? x : 0];
+                    tmem_ld64(lanes + buf * 128 + x * 64, h);
+                    if (masked) {
+                        const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
 #pragma unroll
-                            for (int y = 0; y < 64; ++y)
-                                if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) h[y] = 0xff800000u;   // -inf
-                        }
-                    };
+                        for (int y = 0; y < 64; ++y)
+                            if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) h[y] = 0xff800000u;   // -inf
+                    }
+                };
+                float off = 0.f;
+                if (live) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll kTimes
                     for (int x = 0; x < 2; ++x) {
@@ -635,7 +622,37 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             m = mn;
                         }
                     }
-                    const float off = m == -INFINITY ? 0.f : -m * c;
+                    off = m == -INFINITY ? 0.f : -m * c;
+                }
+                if (masked) {
+                    // value rows past the context: zero those past the length, and those that are not finite
+                    const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
+                    wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
+                    unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (row >> 3) * (C::kBlocks * 1024) + (row & 7) * 128;
+                    // (a bf16 of all-ones exponent carries into bit 15 when 0x80 is added)
+                    uint32_t top = 0;
+                    if (k0 + row >= U.q.ctx && k0 + row < len)
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x) {   // the swizzle's order: no two rows of eight in one bank
+                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4));
+                            top |= ((v.x & 0x7fff7fffu) + 0x00800080u) | ((v.y & 0x7fff7fffu) + 0x00800080u) |
+                                   ((v.z & 0x7fff7fffu) + 0x00800080u) | ((v.w & 0x7fff7fffu) + 0x00800080u);
+                        }
+                    const bool bad = (top & 0x80008000u) != 0;
+                    const uint32_t badw = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0) S.bad[w][tile & 1][quad] = badw;   // the other parity may still be read
+                    // all have looked before anyone zeroes
+                    if (both) named_barrier(1, 256); else named_barrier(2 + w, 128);
+                    if (w == 0 && (bad || k0 + row >= len))
+#pragma unroll 4
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (bits[x] & S.bad[w][tile & 1][x]) poison = NAN;
+                }
+                if (live) {
                     const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll kTimes
