@@ -280,16 +280,24 @@ cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
     return launch_join<T, 2 * kC, kPlainCost>(a, grid, P::kRows, cfg);
 }
 
+template <typename T, int kC>
+cudaError_t launch_plain_r(const AttentionArgs& a, int tall, int sms, cudaStream_t s) {
+    return tall == 4 ? launch_plain_t<T, kC, 4>(a, sms, s) : tall == 2 ? launch_plain_t<T, kC, 2>(a, sms, s) : launch_plain_t<T, kC, 1>(a, sms, s);
+}
+
 template <typename T>
 cudaError_t launch_plain(const AttentionArgs& a, int sms, cudaStream_t s) {
     if (sms <= 0) return cudaErrorNotSupported;
-    // units of 64 rows where the requests have more than 32 a key head on average
-    const bool tall = (long long)a.T * a.group > 32LL * a.R;
+    // Units of 16, 32 or 64 rows, by the requests' rows a key head on average.
+    AttentionArgs b = a;
+    const long long mean = ((long long)a.T * a.group + a.R - 1) / a.R;
+    b.min_steps = 1;
+    const int tall = mean > 32 ? 4 : mean > 16 ? 2 : 1;
     switch ((a.D + 63) / 64) {
-        case 1: return tall ? launch_plain_t<T, 1, 4>(a, sms, s) : launch_plain_t<T, 1, 2>(a, sms, s);
-        case 2: return tall ? launch_plain_t<T, 2, 4>(a, sms, s) : launch_plain_t<T, 2, 2>(a, sms, s);
-        case 3: return tall ? launch_plain_t<T, 3, 4>(a, sms, s) : launch_plain_t<T, 3, 2>(a, sms, s);
-        default: return tall ? launch_plain_t<T, 4, 4>(a, sms, s) : launch_plain_t<T, 4, 2>(a, sms, s);
+        case 1: return launch_plain_r<T, 1>(b, tall, sms, s);
+        case 2: return launch_plain_r<T, 2>(b, tall, sms, s);
+        case 3: return launch_plain_r<T, 3>(b, tall, sms, s);
+        default: return launch_plain_r<T, 4>(b, tall, sms, s);
     }
 }
 

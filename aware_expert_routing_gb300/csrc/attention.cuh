@@ -121,6 +121,7 @@ struct AttentionArgs {
     float2* ml;                // [2 * ranges][rows]
     float* o;                  // [2 * ranges][rows][D]
     int rows;
+    int min_steps;             // fewest steps of a range, on average
     long long wait_cycles;
 };
 

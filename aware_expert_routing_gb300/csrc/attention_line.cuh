@@ -164,7 +164,8 @@ __device__ __forceinline__ void find_start(const AttentionArgs& a, LineStart& S)
         if (w < (int)(threadIdx.x >> 5)) before += t;
         total += t;
     }
-    const int ranges = min((int)gridDim.x, total);
+    // (no range of a few steps where that makes many parts of many rows)
+    const int ranges = min((int)gridDim.x, (total + a.min_steps - 1) / a.min_steps);
     const Line line(total, ranges);
     const int b = line.start(blockIdx.x), e = line.start(blockIdx.x + 1);
     if (threadIdx.x == 0) {

@@ -234,6 +234,20 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(dtype):
     c.check(out, l3)
 
 
+@pytest.mark.parametrize("ctx,n", [([2000, 3500], [20, 30]), ([900, 40, 3000], [9, 1, 20]), ([1500], [3])])
+def test_row_tiles_that_are_not_full_give_the_same_bits(ctx, n):
+    """Rows of a tile past the unit's own hold what earlier calls left there; it must not show in the others."""
+    c = Case(ctx, n, 16, 2, 128, 16, "bf16", True, 31)
+    other = Case([700, 300], [50, 61], 16, 2, 128, 16, "bf16", True, 32, q_scale=30.0)
+    want, l, flags = c.run()
+    assert flags == 0
+    c.check(want, l)
+    for _ in range(20):
+        other.run()
+        got, l2, flags = c.run()
+        assert flags == 0 and torch.equal(got, want) and torch.equal(l, l2)
+
+
 def test_tokens_past_the_last_request_are_not_written():
     c = Case([30, 8], [2, 3], 8, 2, 64, 16, "bf16", False, 13)
     want, l, _ = c.run()
