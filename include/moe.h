@@ -591,16 +591,23 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  *   out        [T][heads][head_dim], dense: sum_j softmax(scale q.k)_j v_j.
  *   lse        [T][heads] fp32, nullable: ln sum_j exp(scale q.k_j).
  * A token that sees nothing gets zeros and an lse of -inf.  Tokens past
- * q_offsets[n_requests] are not written.  What lies in positions that no
- * token of the request sees, and in rows of its pages past its length, has
- * no influence whatever its value.
+ * q_offsets[n_requests] are not written.  What lies in positions that a
+ * token does not see, and in rows of its request's pages past its length,
+ * has no influence on it whatever its value; a token that sees a drafted
+ * token whose value (V) is not finite may become NaN in all components.
  * A request whose length does not fit max_pages, whose page is outside
  * 0..n_pages-1, or whose q_offsets or ctx_len are out of range raises
  * MOE_FLAG_BAD_INDEX; its output is unspecified, other requests are not
- * affected.
+ * affected.  A wait that passes moe_set_wait_timeout_us raises
+ * MOE_FLAG_WAIT_TIMEOUT; the call's output is not valid then, and the
+ * workspace is ready for the next call.
+ * Lengths, offsets, table and mask are read on the device, so a captured
+ * call follows their contents.  Results repeat bit for bit.
  * Products and sums are fp32; bf16: the exponentials are rounded to bf16
- * before the product with V (tensor cores), their sum is not.
- * n_requests at most MOE_MAX_REQUESTS.
+ * before the product with V, their sum is not (tensor cores: heads of 64 or
+ * 128 and pages that are a multiple of 8 and divide 128 or are a multiple of
+ * it; other heads and pages, and fp32, run on CUDA cores).
+ * n_requests at most MOE_MAX_REQUESTS, max_pages * page_size at most 2^30.
  */
 typedef struct {
     int32_t T;
