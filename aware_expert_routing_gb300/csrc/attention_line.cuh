@@ -2,10 +2,11 @@
 // the kernel that joins what the shares cut.
 //
 // A unit of work is (request, key head, tile of query rows).  Its key tiles,
-// one step each after kUnitCost steps for what a unit costs besides (queries,
-// first scores, result), follow one another in one line with those of all
-// other units, and the line is cut into equal stretches ("ranges"), one per
-// CTA.  So ragged lengths balance, one long request is spread over all CTAs,
+// one step each, and kUnitCost steps for what a unit costs besides (queries,
+// first scores, result; some before the tiles, some after them, so that a cut
+// close to a unit's end moves to it), follow one another in one line with
+// those of all other units, and the line is cut into equal stretches
+// ("ranges"), one per CTA.  So ragged lengths balance, one long request is spread over all CTAs,
 // and the lengths are read on the device.  A unit that a cut goes through
 // leaves partial results (AttentionLayout) in each of its ranges.
 #pragma once
@@ -21,6 +22,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// Of a unit's cost, the steps before its key tiles (all before: 27.5 against
+// 27.1 us for 16 trees of 16 to 4000).
+__host__ __device__ constexpr int steps_before(int cost) { return cost - cost * 2 / 5; }
 
 // The line of `total` steps in `ranges` equal stretches (the first ones a
 // step longer where it does not divide).
@@ -76,8 +81,9 @@ struct LineWalk {
     __device__ __forceinline__ bool part(int off) {
         const int take = min(q.nkt + kUnitCost - off, left);
         left -= take;
-        kt = max(0, off - kUnitCost);
-        nk = max(0, off + take - kUnitCost) - kt;
+        constexpr int kBefore = steps_before(kUnitCost);
+        kt = min(max(0, off - kBefore), q.nkt);
+        nk = min(max(0, off + take - kBefore), q.nkt) - kt;
         return nk > 0;
     }
     __device__ __forceinline__ bool start(const AttentionArgs& a, const LineStart& S) {
@@ -198,7 +204,7 @@ __device__ __forceinline__ void find_start(const AttentionArgs& a, LineStart& S)
         rec.line_q = line.q;
         rec.line_rem = line.rem;
         a.plan[blockIdx.x] = rec;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.page_table + (size_t)r * a.max_pages + max(0, off - kUnitCost) * kKeys / a.page_size));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.page_table + (size_t)r * a.max_pages + min(max(0, off - steps_before(kUnitCost)), q.nkt - 1) * kKeys / a.page_size));
     }
 }
 
@@ -239,8 +245,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     const Line line(rec);
     auto start = [&](int x) { return line.start(x); };
     // the unit's stretch of the line: its start, its first key tile, its end
-    const int u0 = start(c) - rec.off, k0 = u0 + kUnitCost, u1 = k0 + rec.nkt;
-    if (start(c) <= k0 || start(c - 1) > k0) return;
+    const int u0 = start(c) - rec.off, k0 = u0 + steps_before(kUnitCost), u1 = k0 + rec.nkt;
+    if (start(c) <= k0 || start(c) >= u1 || start(c - 1) > k0) return;
     const int group = a.group;
     const int nrows = min(unit_rows, rec.n * group - rec.rt * unit_rows);
     if ((int)blockIdx.y * kJoinRows >= nrows) return;

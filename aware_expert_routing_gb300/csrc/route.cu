@@ -120,6 +120,7 @@ struct RouteSmem {
 
 // Writes the routing of token i (this CTA's token il): lane r < cnt holds
 // slot r (expert myid, weight w).
+template <bool kGiven = false>   // the experts and weights are there already
 __device__ __forceinline__ void store_token(const RouteArgs& a, RouteSmem& sm, int i, int il, int lane, int cnt,
                                             int myid, float w) {
     if (lane == 0) a.nused[i] = cnt;
@@ -127,8 +128,10 @@ __device__ __forceinline__ void store_token(const RouteArgs& a, RouteSmem& sm, i
     if (lane < a.kslots) {
         const size_t q = (size_t)i * a.kslots + lane;
         const bool used = lane < cnt;
-        a.idx[q] = used ? myid : -1;
-        a.w[q] = used ? w : 0.f;
+        if (!kGiven) {
+            a.idx[q] = used ? myid : -1;
+            a.w[q] = used ? w : 0.f;
+        }
         sm.sidx[il * a.kslots + lane] = used ? myid : -1;
         if (used) atomicOr(&sm.bits[myid], 1u << il);
         else a.pos_of[q] = -1;
@@ -152,9 +155,11 @@ __host__ __device__ constexpr int select_words(int N) { return (N + 31) / 32 * 3
 // (moe_select_params), for one token by one warp; lane l holds experts l,
 // l + 32, ...  `row` is the token's scores, `scratch` the warp's words of
 // select_words(N) (with groups).
+// Returns the number of experts; lane r below it gets slot r's expert and
+// weight.
 template <int NPL>
-__device__ __forceinline__ void select_token(const RouteArgs& a, const SelectArgs& sel, RouteSmem& sm, uint32_t* scratch,
-                                             const float* row, int i, int il, int lane, bool& nonfinite) {
+__device__ __forceinline__ int select_token(const RouteArgs& a, const SelectArgs& sel, uint32_t* scratch, const float* row,
+                                            int lane, bool& nonfinite, int& myid, float& w) {
     const int N = a.N;
     float x[NPL], top = -INFINITY;
 #pragma unroll
@@ -236,7 +241,8 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const SelectArg
         }
     }
     uint32_t taken = 0;
-    int myid = -1, n = 0;
+    int n = 0;
+    myid = -1;
     for (int r = 0; r < a.k; ++r) {
         int id;
         const uint32_t m = warp_best<NPL>(kv, taken, lane, id);
@@ -245,13 +251,13 @@ __device__ __forceinline__ void select_token(const RouteArgs& a, const SelectArg
         if (lane == r) myid = id;
         n = r + 1;
     }
-    float w = lane < n ? score(row[myid]) : 0.f;
+    w = lane < n ? score(row[myid]) : 0.f;
     if (sel.renorm) {
         const float z = warp_sum(w);
         w = z > 0.f ? w / z : 0.f;
     }
-    if (lane == 0 && a.n_base) a.n_base[i] = n;
-    store_token(a, sm, i, il, lane, n, myid, w * sel.scale);
+    w *= sel.scale;
+    return n;
 }
 
 // Publishes the OEA union S_base: lane j stores word j (bit b: expert
@@ -291,8 +297,9 @@ __device__ __forceinline__ void route_prepare(const RouteArgs& a, unsigned char*
 // cluster, from the scores at `logits` (global or shared memory).  Prepared:
 // the caller has run route_prepare and synchronised the CTA after its
 // dependency wait.
-// kSelect: moe_select_params instead of plain top-k or OEA.
-template <int NPL, bool kPrepared, bool kSelect>
+// kPick: where the experts come from.
+enum { kPlain, kSelect, kGiven };   // plain top-k or OEA; moe_select_params; routing.expert_idx, already written
+template <int NPL, bool kPrepared, int kPick>
 __device__ __forceinline__ void route_body(const RouteArgs& a, const SelectArgs& sel, const float* logits, unsigned char* smem_raw,
                                            uint32_t* scratch, const uint32_t rank, const uint32_t ncta) {
     const int nthreads = blockDim.x;
@@ -322,7 +329,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const SelectArgs&
     }
 
     bool nonfinite = false;
-    const bool oea = !kSelect && a.mode == MOE_MODE_OEA;
+    const bool oea = kPick == kPlain && a.mode == MOE_MODE_OEA;
     const bool keep_keys = te - tb <= nwarps;   // one token per warp: keys and picks stay in registers
     uint32_t kv[NPL];
     // Phase-1 picks of this warp's token (used by phase 2 when keep_keys).
@@ -333,12 +340,21 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const SelectArgs&
     // ---- plain top-k, or OEA phase 1 (baseline and union) ------------------
     for (int i = tb + warp; i < te; i += nwarps) {
         const int il = i - tb;
-        if (kSelect && i < a.B_valid) {
-            select_token<NPL>(a, sel, sm, scratch + warp * select_words(N), logits + (size_t)i * N, i, il, lane, nonfinite);
+        if (kPick == kGiven) {
+            const int id = lane < a.kslots ? a.idx[(size_t)i * a.kslots + lane] : -1;
+            store_token<true>(a, sm, i, il, lane, __popc(__ballot_sync(kFull, id >= 0)), id, 0.f);
+            continue;
+        }
+        if (kPick == kSelect && i < a.B_valid) {
+            int id;
+            float w;
+            const int n = select_token<NPL>(a, sel, scratch + warp * select_words(N), logits + (size_t)i * N, lane, nonfinite, id, w);
+            if (lane == 0 && a.n_base) a.n_base[i] = n;
+            store_token(a, sm, i, il, lane, n, id, w);
             continue;
         }
         load_keys<NPL>(logits + (size_t)i * N, N, lane, kv, nonfinite);
-        if (kSelect || i >= a.B_valid) {   // padding token: selects nothing
+        if (kPick != kPlain || i >= a.B_valid) {   // padding token: selects nothing
             if (lane == 0) {
                 sm.snb[il] = 0;
                 if (a.n_base && !oea) a.n_base[i] = 0;   // OEA: after S_base is published
@@ -581,11 +597,11 @@ __host__ __device__ constexpr size_t route_smem_bytes(int N, int kslots) {
     return 4 * 32 * 4 + 3 * (size_t)N * 4 + 32 * (size_t)kslots * 4;
 }
 
-template <int NPL, bool kSelect>
+template <int NPL, int kPick>
 __global__ void route_kernel(RouteArgs a, SelectArgs sel) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     uint32_t* scratch = reinterpret_cast<uint32_t*>(smem_raw + route_smem_bytes(a.N, a.kslots));
-    route_body<NPL, false, kSelect>(a, sel, a.logits, smem_raw, scratch, cluster_ctarank(), gridDim.x);   // the whole grid is one cluster
+    route_body<NPL, false, kPick>(a, sel, a.logits, smem_raw, scratch, cluster_ctarank(), gridDim.x);   // the whole grid is one cluster
 }
 
 // ---- scores and routing in one cluster (bf16, up to 32 tokens, N <= 128) ----
@@ -627,7 +643,7 @@ __host__ __device__ constexpr size_t fused_smem_bytes(int N, int kslots) {
            (size_t)kFusedWarps * 512 * 4;
 }
 
-template <int NPL, bool kSelect>
+template <int NPL, int kPick>
 __global__ void __launch_bounds__(kFusedWarps * 32, 1) route_fused_kernel(RouterArgs r, RouteArgs a, SelectArgs sel) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const size_t rsm = (route_smem_bytes(a.N, a.kslots) + 15) & ~size_t(15);
@@ -710,10 +726,10 @@ __global__ void __launch_bounds__(kFusedWarps * 32, 1) route_fused_kernel(Router
     if (rank != 0) return;
     // the routing reads every argument from the kernel's parameters and the
     // scores from shared memory
-    route_body<NPL, true, kSelect>(a, sel, lg, smem_raw, reinterpret_cast<uint32_t*>(red), 0u, 1u);
+    route_body<NPL, true, kPick>(a, sel, lg, smem_raw, reinterpret_cast<uint32_t*>(red), 0u, 1u);
 }
 
-template <int NPL, bool kSelect>
+template <int NPL, int kPick>
 cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int ncta = (a.N + 15) / 16;
     const size_t smem = fused_smem_bytes(a.N, a.kslots);
@@ -723,7 +739,7 @@ cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, const 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(route_fused_kernel<NPL, kSelect>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
+        e = cudaFuncSetAttribute(route_fused_kernel<NPL, kPick>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
@@ -741,15 +757,39 @@ cudaError_t launch_route_fused_t(const RouterArgs& r, const RouteArgs& a, const 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ncta > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, route_fused_kernel<NPL, kSelect>, r, a, sel);
+    return cudaLaunchKernelEx(&cfg, route_fused_kernel<NPL, kPick>, r, a, sel);
 }
 
-template <int NPL, bool kSelect>
+// Selection alone, a warp per token, spread over the SMs.
+constexpr int kSelectWarps = 4;
+
+template <int NPL>
+__global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(RouteArgs a, SelectArgs sel) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * kSelectWarps + warp;
+    if (i >= a.B) return;
+    int id = -1, n = 0;
+    float w = 0.f;
+    bool nonfinite = false;
+    if (i < a.B_valid)
+        n = select_token<NPL>(a, sel, reinterpret_cast<uint32_t*>(smem_raw) + warp * select_words(a.N), a.logits + (size_t)i * a.N,
+                              lane, nonfinite, id, w);
+    if (lane == 0 && a.n_base) a.n_base[i] = n;
+    if (lane < a.kslots) {
+        a.idx[(size_t)i * a.kslots + lane] = lane < n ? id : -1;
+        a.w[(size_t)i * a.kslots + lane] = lane < n ? w : 0.f;
+    }
+    if (__any_sync(kFull, nonfinite) && lane == 0) raise_flag(a.flags, kFlagNonFinite);
+}
+
+template <int NPL, int kPick>
 cudaError_t launch_route_t(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int threads = NPL <= 8 ? 1024 : 512;
     const int ncta = a.B > 0 ? (a.B + 31) / 32 : 1;
     size_t smem = route_smem_bytes(a.N, a.kslots);
-    if (kSelect && sel.n_group > 1) {
+    if (kPick == kSelect && sel.n_group > 1) {
         smem += (size_t)threads / 32 * select_words(a.N) * 4;
         static bool attr_set[64] = {};
         int dev = 0;
@@ -757,7 +797,7 @@ cudaError_t launch_route_t(const RouteArgs& a, const SelectArgs& sel, cudaStream
         if (e != cudaSuccess) return e;
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         if (smem > 48 * 1024 && !attr_set[dev]) {
-            e = cudaFuncSetAttribute(route_kernel<NPL, kSelect>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
+            e = cudaFuncSetAttribute(route_kernel<NPL, kPick>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_cap());
             if (e != cudaSuccess) return e;
             attr_set[dev] = true;
         }
@@ -777,7 +817,7 @@ cudaError_t launch_route_t(const RouteArgs& a, const SelectArgs& sel, cudaStream
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ncta > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, route_kernel<NPL, kSelect>, a, sel);
+    return cudaLaunchKernelEx(&cfg, route_kernel<NPL, kPick>, a, sel);
 }
 
 }  // namespace
@@ -788,33 +828,67 @@ bool route_fused_supported(int dtype, int B, int N, int kslots) {
 
 namespace {
 
-template <bool kSelect>
+template <int kPick>
 cudaError_t launch_route_fused_s(const RouterArgs& r, const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int nw = (a.N + 31) / 32;
-    if (nw <= 1) return launch_route_fused_t<1, kSelect>(r, a, sel, s);
-    if (nw <= 2) return launch_route_fused_t<2, kSelect>(r, a, sel, s);
-    return launch_route_fused_t<4, kSelect>(r, a, sel, s);
+    if (nw <= 1) return launch_route_fused_t<1, kPick>(r, a, sel, s);
+    if (nw <= 2) return launch_route_fused_t<2, kPick>(r, a, sel, s);
+    return launch_route_fused_t<4, kPick>(r, a, sel, s);
 }
 
-template <bool kSelect>
+template <int kPick>
 cudaError_t launch_route_s(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
     const int nw = (a.N + 31) / 32;
-    if (nw <= 1) return launch_route_t<1, kSelect>(a, sel, s);
-    if (nw <= 2) return launch_route_t<2, kSelect>(a, sel, s);
-    if (nw <= 4) return launch_route_t<4, kSelect>(a, sel, s);
-    if (nw <= 8) return launch_route_t<8, kSelect>(a, sel, s);
-    if (nw <= 16) return launch_route_t<16, kSelect>(a, sel, s);
-    return launch_route_t<32, kSelect>(a, sel, s);
+    if (nw <= 1) return launch_route_t<1, kPick>(a, sel, s);
+    if (nw <= 2) return launch_route_t<2, kPick>(a, sel, s);
+    if (nw <= 4) return launch_route_t<4, kPick>(a, sel, s);
+    if (nw <= 8) return launch_route_t<8, kPick>(a, sel, s);
+    if (nw <= 16) return launch_route_t<16, kPick>(a, sel, s);
+    return launch_route_t<32, kPick>(a, sel, s);
 }
+
+template <int NPL>
+cudaError_t launch_select_t(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.B + kSelectWarps - 1) / kSelectWarps);
+    cfg.blockDim = dim3(kSelectWarps * 32);
+    cfg.dynamicSmemBytes = sel.n_group > 1 ? (size_t)kSelectWarps * select_words(a.N) * 4 : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, select_kernel<NPL>, a, sel);
+}
+
+cudaError_t launch_select(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
+    const int nw = (a.N + 31) / 32;
+    if (nw <= 1) return launch_select_t<1>(a, sel, s);
+    if (nw <= 2) return launch_select_t<2>(a, sel, s);
+    if (nw <= 4) return launch_select_t<4>(a, sel, s);
+    if (nw <= 8) return launch_select_t<8>(a, sel, s);
+    if (nw <= 16) return launch_select_t<16>(a, sel, s);
+    return launch_select_t<32>(a, sel, s);
+}
+
+// Tokens from which the selection has a kernel of its own: in the cluster's
+// few SMs, 32 warps each work through it (256 experts in 8 groups, k 8; one
+// kernel / two: 4 tokens 7.2 / 7.7 us, 8 7.7 / 7.9, 16 8.7 / 7.9, 32 11.5 / 8.1,
+// 256 12.6 / 9.4).
+constexpr int kOwnSelection = 12;
 
 }  // namespace
 
 cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
-    return sel ? launch_route_fused_s<true>(r, a, *sel, s) : launch_route_fused_s<false>(r, a, SelectArgs{}, s);
+    return sel ? launch_route_fused_s<kSelect>(r, a, *sel, s) : launch_route_fused_s<kPlain>(r, a, SelectArgs{}, s);
 }
 
 cudaError_t launch_route(const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
-    return sel ? launch_route_s<true>(a, *sel, s) : launch_route_s<false>(a, SelectArgs{}, s);
+    if (!sel) return launch_route_s<kPlain>(a, SelectArgs{}, s);
+    if (a.B < kOwnSelection) return launch_route_s<kSelect>(a, *sel, s);
+    const cudaError_t e = launch_select(a, *sel, s);
+    return e == cudaSuccess ? launch_route_s<kGiven>(a, *sel, s) : e;
 }
 
 }  // namespace moe
