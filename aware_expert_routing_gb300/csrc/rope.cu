@@ -7,6 +7,7 @@
 // so a query's product with a key depends on the distance of their
 // positions only.
 #include <cmath>
+#include <type_traits>
 
 #include "attention.cuh"
 
@@ -106,11 +107,10 @@ template <> struct Vec<__nv_bfloat16> {
 // y, some of its rows: query heads, key heads, value heads); threadIdx.x is
 // the place in a row: a word of each half of the rotated part (half layout),
 // or a word.  It keeps its cosines and sines for all rows it goes through.
-// Five blocks an SM (48 registers): 60.5 us for 16000 tokens of 32 + 2 x 4
-// heads of 128 in bf16, 5.6 TB/s; two rows a thread at once, or four blocks, 65
-// to 68; six blocks spill, 65.
-template <typename T, bool kPairs>
-__global__ void __launch_bounds__(256, 5) append_kernel(const AppendArgs a) {
+// kMany: small blocks, see kManyTokens.  Registers decide how many words are
+// under way: with 84 of them 16000 tokens take 79 us, with 64 67, with 48 60.
+template <typename T, bool kPairs, bool kMany>
+__global__ void __launch_bounds__(kMany ? 64 : 256, kMany ? 24 : 5) append_kernel(const AppendArgs a) {
     constexpr int N = Vec<T>::kN;
     const int t = blockIdx.x, x = threadIdx.x, nx = blockDim.x, D = a.D;
     const int half = a.rot / 2;
@@ -224,6 +224,12 @@ __global__ void append_any_kernel(const AppendArgs a) {
     }
 }
 
+// Tokens from which blocks are small (64 threads, about five rows each) and
+// their number hides the latency; below, more threads share a token.  bf16, 32
+// + 2 x 4 heads of 128: 16000 tokens 59.6 (256 threads) against 52.1 us, 6.4
+// TB/s; 8000 31.9 / 29.7; 4000 18.2 / 18.3; 256 of 64 + 2 x 4 heads 3.1 / 4.2.
+constexpr int kManyTokens = 4000;
+
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     constexpr int N = Vec<T>::kN;
@@ -243,13 +249,19 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     const bool pairs = a.interleaved || a.rot == 0;
     const int nx = pairs ? a.D / N : a.rot / 2 / N + (a.D - a.rot) / N;
     const int rows = a.heads + 2 * a.kv_heads;
-    // Few tokens: a row per thread, spread over blocks.  Many: each thread
-    // goes through several rows with the same cosines and sines.
-    const int most = 256 / nx, each = (rows + most - 1) / most;
+    const bool many = a.T >= kManyTokens && nx <= 64;
+    const int most = (many ? 64 : 256) / nx, each = (rows + most - 1) / most;
     const int ny = (rows + each - 1) / each;
+    // few tokens: a row per thread, spread over blocks
     cfg.gridDim = dim3(a.T, a.T <= 304 ? each : 1);
     cfg.blockDim = dim3(nx, ny);
-    return pairs ? cudaLaunchKernelEx(&cfg, append_kernel<T, true>, a) : cudaLaunchKernelEx(&cfg, append_kernel<T, false>, a);
+    auto launch = [&](auto pair, auto lot) {
+        return cudaLaunchKernelEx(&cfg, append_kernel<T, decltype(pair)::value, decltype(lot)::value>, a);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (pairs) return many ? launch(Yes{}, Yes{}) : launch(Yes{}, No{});
+    return many ? launch(No{}, Yes{}) : launch(No{}, No{});
 }
 
 }  // namespace

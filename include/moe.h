@@ -588,6 +588,7 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  *              j % 32 of word j / 32 of its row is set (a draft tree: its
  *              ancestors and itself); tokens past 32 * mask_words are not
  *              seen.  NULL: token i sees tokens 0..i.
+ *   scale      positive and finite.
  *   out        [T][heads][head_dim], dense: sum_j softmax(scale q.k)_j v_j.
  *   lse        [T][heads] fp32, nullable: ln sum_j exp(scale q.k_j).
  * A token that sees nothing gets zeros and an lse of -inf.  Tokens past
