@@ -653,9 +653,12 @@ def moe_attention_workspace_bytes(T: int, heads: int, cache: KvCache) -> int:
 
 
 def alloc_attention_workspace(T: int, heads: int, cache: KvCache, device) -> torch.Tensor:
-    """A zero-filled workspace for moe_kv_append and moe_tree_attention of up
-    to T tokens with `heads` query heads on this cache."""
-    return torch.zeros(moe_attention_workspace_bytes(T, heads, cache), dtype=torch.uint8, device=device)
+    """A workspace (its flag word cleared) for moe_kv_append and
+    moe_tree_attention of up to T tokens with `heads` query heads on this
+    cache."""
+    ws = torch.empty(moe_attention_workspace_bytes(T, heads, cache), dtype=torch.uint8, device=device)
+    ws[:ATTENTION_WORKSPACE_MIN].zero_()
+    return ws
 
 
 def moe_kv_append(q, k, v, rope, positions, slots, cache: KvCache, q_out, workspace: torch.Tensor,

@@ -553,7 +553,7 @@ moe_status moe_rope_table(const moe_rope_params *params, int32_t n_pos, float *t
  *   q_out     rotated queries; may be q itself with the same distances.
  * A pair (a, b) becomes (a cos - b sin, b cos + a sin) in fp32, rounded
  * once.  The workspace holds the flag word: MOE_ATTENTION_WORKSPACE_MIN
- * bytes (or more), zero-filled once before its first use.
+ * bytes (or more), these zero-filled once before its first use.
  */
 typedef struct {
     int32_t T;
@@ -620,7 +620,8 @@ typedef struct {
 
 /* Workspace for up to T tokens of `heads` query heads on this cache (its
  * buffers are not read); 0 if the arguments are invalid.  256-byte aligned,
- * zero-filled once before its first use.  It serves moe_kv_append too. */
+ * its first MOE_ATTENTION_WORKSPACE_MIN bytes zero-filled once before its
+ * first use.  It serves moe_kv_append too. */
 size_t moe_attention_workspace_bytes(int32_t T, int32_t heads, const moe_kv_cache *cache);
 
 moe_status moe_tree_attention(const void *q, const int32_t *q_offsets, const int32_t *ctx_len, const uint32_t *mask,
