@@ -10,7 +10,10 @@
 // tensor cores (attention_tc.cu) do not: fp32, and bf16 heads or pages of
 // other sizes.  fp32 has no tensor-core path that keeps fp32's accuracy, so its
 // bound is the FMA rate (74 TFLOP/s at 1.9 GHz) from about 11 query rows a key
-// head on, and the cache's bytes below.
+// head on, and the cache's bytes below.  Measured, 4 trees of 7 tokens up to
+// 2000 positions, 8 + 2 heads of 64: 15.0 us, of which the bytes would take 0.6;
+// at this length the steps of one unit (lengths, table, tile, scores, softmax,
+// values) wait for one another.
 #include <type_traits>
 
 #include "attention_line.cuh"
@@ -23,18 +26,21 @@ namespace {
 
 constexpr int kPlainCost = 2;   // a unit's own cost, in key tiles
 
-// kC = ceil(D / 64), kR: query rows per thread.  256 threads as 16 x 16: for
-// the scores, thread (ty, tx) has rows ty kR .. and keys tx, tx + 16, ...; for
-// the products with V, the same rows and components 4 tx .. of every 64, so a
-// row's maximum, sum and correction stay with its 16 threads (half a warp).
+// kC = ceil(D / 64), kR: query rows per thread, kS: shares of a tile's keys.
+// 256 threads as kS shares x (16 / kS) x 16: for the scores, thread (z, ty, tx)
+// has rows ty kR .. and keys tx, tx + 16, ... of share z; for the products with
+// V, the same rows, its share's keys and components 4 tx .. of every 64.  So a
+// row's maximum, sum and correction in a share stay with 16 threads (half a
+// warp), and shares meet once, at the unit's end.
 // Tiles of keys and values arrive by asynchronous copies one tile ahead, in
 // the cache's own type; rows are padded by 16 bytes, which puts eight rows'
 // 16-byte words in different banks.
-template <typename T, int kC, int kR>
+template <typename T, int kC, int kR, int kS>
 struct Plain {
-    static constexpr int kRows = 16 * kR;
+    static constexpr int kRows = 16 / kS * kR;
     static constexpr int kKeys = kC == 1 ? 64 : 32;
     static constexpr int kPad = 16 / (int)sizeof(T);
+    static_assert(kS == 1 || (kKeys % (16 * kS) == 0 && 4 * kS * kRows <= 2 * kKeys * (int)sizeof(T)), "the shares' sums fit where the keys were");
     static size_t smem(int D) {
         return 4 * (size_t)kKeys * (D + kPad) * sizeof(T) + (size_t)kRows * (D + 4) * 4 + (size_t)kRows * (kKeys + 4) * 4 +
                2 * kKeys * sizeof(long long) + sizeof(LineStart);
@@ -49,11 +55,11 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-template <typename T, int kC, int kR>
+template <typename T, int kC, int kR, int kS>
 __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArgs a) {
-    using P = Plain<T, kC, kR>;
+    using P = Plain<T, kC, kR, kS>;
     using Walk = LineWalk<P::kRows, P::kKeys, kPlainCost>;
-    constexpr int kRows = P::kRows, kKeys = P::kKeys, kJ = kKeys / 16;
+    constexpr int kRows = P::kRows, kKeys = P::kKeys, kShare = kKeys / kS, kJ = kShare / 16;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const int D = a.D, ld = D + P::kPad, group = a.group;
     T* ks = reinterpret_cast<T*>(smem_raw);                      // [2][kKeys][ld]
@@ -62,7 +68,7 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
     float* ps = qs + kRows * (D + 4);                            // [kRows][kKeys + 4]
     long long* row_at = reinterpret_cast<long long*>(ps + kRows * (kKeys + 4));   // [2][kKeys]: place in the cache, -1: none
     LineStart& S = *reinterpret_cast<LineStart*>(row_at + 2 * kKeys);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid & 15, ty = (tid >> 4) % (16 / kS), key0 = (tid >> 4) / (16 / kS) * kShare;
     const float c = a.scale * 1.4426950408889634f;   // scores to powers of two
 
     prefetch_tables(a);
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
             for (int i = 0; i < kR; ++i)
 #pragma unroll
                 for (int y = 0; y < kJ; ++y) s[i][y] = 0.f;
-            const T* kt = ks + (size_t)(j & 1) * kKeys * ld;
+            const T* kt = ks + ((size_t)(j & 1) * kKeys + key0) * ld;
 #pragma unroll 2
             for (int d = 0; d < D; d += 4) {
                 float4 k[kJ];
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
                 if (masked) {
 #pragma unroll
                     for (int y = 0; y < kJ; ++y) {
-                        const int d = k0 + tx + 16 * y - ctx;   // which drafted token; below 0: context
+                        const int d = k0 + key0 + tx + 16 * y - ctx;   // which drafted token; below 0: context
                         bool seen = d < 0;
                         if (d >= 0 && d < n && ty * kR + i < nrows)
                             seen = a.mask ? d < 32 * a.mask_words &&
@@ -183,11 +189,9 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
                 for (int y = 0; y < kJ; ++y) {
                     const float p = ex2(s[i][y] - sub);
                     sum += p;
-                    ps[(ty * kR + i) * (kKeys + 4) + tx + 16 * y] = p;
+                    ps[(ty * kR + i) * (kKeys + 4) + key0 + tx + 16 * y] = p;
                 }
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                l[i] = l[i] * f + sum;
+                l[i] = l[i] * f + sum;   // this thread's keys; the 16 threads' sums meet at the end
                 m[i] = mn;
 #pragma unroll
                 for (int y = 0; y < kC; ++y)
@@ -196,13 +200,13 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
             }
             __syncwarp();   // a row's P is written and read by the same warp
             // ---- O += P V; where a mask hides a value, it is not multiplied (it may be anything) ----
-            const T* vt = vs + (size_t)(j & 1) * kKeys * ld;
+            const T* vt = vs + ((size_t)(j & 1) * kKeys + key0) * ld;
             auto product = [&](auto hide) {
 #pragma unroll 2
-                for (int x = 0; x < kKeys; x += 4) {
+                for (int x = 0; x < kShare; x += 4) {
                     float4 p[kR];
 #pragma unroll
-                    for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(ps + (ty * kR + i) * (kKeys + 4) + x);
+                    for (int i = 0; i < kR; ++i) p[i] = *reinterpret_cast<const float4*>(ps + (ty * kR + i) * (kKeys + 4) + key0 + x);
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
 #pragma unroll
@@ -228,29 +232,70 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
         const bool whole = W.nk == W.q.nkt;
         const int slot = 2 * blockIdx.x + (W.first ? 0 : 1);
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            const int row = ty * kR + i, gr = r0 + row;
-            if (row >= nrows) continue;
-            const size_t orow = (size_t)(W.q.t0 + gr / group) * a.heads + W.h * group + gr % group;
+        for (int i = 0; i < kR; ++i)
 #pragma unroll
-            for (int y = 0; y < kC; ++y) {
-                if (tx * 4 + 64 * y >= D) continue;
-                const float4 v = make_float4(o[i][y][0], o[i][y][1], o[i][y][2], o[i][y][3]);
-                if (whole) store_row(static_cast<T*>(a.out) + orow * D + tx * 4 + 64 * y, v, l[i]);
-                else reinterpret_cast<float4*>(a.o)[((size_t)slot * a.rows + (row & ~31)) * (D / 4) + (tx + 16 * y) * 32 + (row & 31)] = v;
+            for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        auto put = [&](int row, int ch, float4 v, float rm, float rl) {   // components 4 ch .. of a row
+            const int gr = r0 + row;
+            const size_t orow = (size_t)(W.q.t0 + gr / group) * a.heads + W.h * group + gr % group;
+            if (whole) store_row(static_cast<T*>(a.out) + orow * D + ch * 4, v, rl);
+            else reinterpret_cast<float4*>(a.o)[((size_t)slot * a.rows + (row & ~31)) * (D / 4) + ch * 32 + (row & 31)] = v;
+            if (ch == 0) {
+                if (!whole) a.ml[(size_t)slot * a.rows + row] = make_float2(rm, rl);
+                else if (a.lse) a.lse[orow] = rl == 0.f ? -INFINITY : (rm + log2f(rl)) * 0.6931471805599453f;
             }
-            if (tx == 0) {
-                if (!whole) a.ml[(size_t)slot * a.rows + row] = make_float2(m[i], l[i]);
-                else if (a.lse) a.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+        };
+        if (kS == 1) {
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                const int row = ty * kR + i;
+                if (row >= nrows) continue;
+#pragma unroll
+                for (int y = 0; y < kC; ++y)
+                    if (tx * 4 + 64 * y < D) put(row, tx + 16 * y, make_float4(o[i][y][0], o[i][y][1], o[i][y][2], o[i][y][3]), m[i], l[i]);
+            }
+        } else {
+            // the shares' sums meet where the keys were: [kS][kRows][D], and
+            // their maxima and sums [kS][kRows] where the values were
+            float* os = reinterpret_cast<float*>(ks);
+            float2* mls = reinterpret_cast<float2*>(vs);
+            const int z = key0 / kShare;
+            __syncthreads();   // the last tile's keys and values have been read
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                const int row = z * kRows + ty * kR + i;
+#pragma unroll
+                for (int y = 0; y < kC; ++y)
+                    if (tx * 4 + 64 * y < D)
+                        *reinterpret_cast<float4*>(os + row * D + tx * 4 + 64 * y) = make_float4(o[i][y][0], o[i][y][1], o[i][y][2], o[i][y][3]);
+                if (tx == 0) mls[row] = make_float2(m[i], l[i]);
+            }
+            __syncthreads();
+            for (int x = tid; x < nrows * (D / 4); x += 256) {
+                const int row = x / (D / 4), ch = x - row * (D / 4);
+                float rm = -INFINITY, rl = 0.f;
+#pragma unroll
+                for (int y = 0; y < kS; ++y) rm = fmaxf(rm, mls[y * kRows + row].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < kS; ++y) {
+                    const float2 e = mls[y * kRows + row];
+                    if (e.y == 0.f) continue;   // saw nothing; a NaN goes on
+                    const float f = ex2(e.x - rm);
+                    const float4 w = *reinterpret_cast<const float4*>(os + (y * kRows + row) * D + ch * 4);
+                    rl = fmaf(f, e.y, rl);
+                    v = make_float4(fmaf(f, w.x, v.x), fmaf(f, w.y, v.y), fmaf(f, w.z, v.z), fmaf(f, w.w, v.w));
+                }
+                put(row, ch, v, rm, rl);
             }
         }
         __syncthreads();   // the next unit overwrites the queries and the tiles
     }
 }
 
-template <typename T, int kC, int kR>
+template <typename T, int kC, int kR, int kS>
 cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
-    using P = Plain<T, kC, kR>;
+    using P = Plain<T, kC, kR, kS>;
     const size_t smem = P::smem(a.D);
     static bool attr_set[64] = {};
     int dev = 0;
@@ -258,7 +303,7 @@ cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(attention_plain_kernel<T, kC, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(attention_plain_kernel<T, kC, kR, kS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)P::smem(64 * kC));
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
@@ -275,14 +320,19 @@ cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, attention_plain_kernel<T, kC, kR>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, attention_plain_kernel<T, kC, kR, kS>, a)) != cudaSuccess) return e;
     if ((long long)a.max_pages * a.page_size <= P::kKeys || grid < 2) return cudaSuccess;   // no unit is cut
     return launch_join<T, 2 * kC, kPlainCost>(a, grid, P::kRows, cfg);
 }
 
 template <typename T, int kC>
-cudaError_t launch_plain_r(const AttentionArgs& a, int tall, int sms, cudaStream_t s) {
-    return tall == 4 ? launch_plain_t<T, kC, 4>(a, sms, s) : tall == 2 ? launch_plain_t<T, kC, 2>(a, sms, s) : launch_plain_t<T, kC, 1>(a, sms, s);
+cudaError_t launch_plain_r(const AttentionArgs& a, int rows, int sms, cudaStream_t s) {
+    constexpr int kS = kC == 1 ? 4 : 2;   // shares of 16 keys
+    if (rows > 32) return launch_plain_t<T, kC, 4, 1>(a, sms, s);
+    if (rows > 16) return launch_plain_t<T, kC, 2, 1>(a, sms, s);
+    if (rows > 8) return launch_plain_t<T, kC, kS, kS>(a, sms, s);
+    if (rows > 4 || kS == 2) return launch_plain_t<T, kC, kS / 2, kS>(a, sms, s);
+    return launch_plain_t<T, kC, 1, kS>(a, sms, s);
 }
 
 template <typename T>
@@ -292,12 +342,12 @@ cudaError_t launch_plain(const AttentionArgs& a, int sms, cudaStream_t s) {
     AttentionArgs b = a;
     const long long mean = ((long long)a.T * a.group + a.R - 1) / a.R;
     b.min_steps = 1;
-    const int tall = mean > 32 ? 4 : mean > 16 ? 2 : 1;
+    const int rows = mean > 64 ? 64 : (int)mean;
     switch ((a.D + 63) / 64) {
-        case 1: return launch_plain_r<T, 1>(b, tall, sms, s);
-        case 2: return launch_plain_r<T, 2>(b, tall, sms, s);
-        case 3: return launch_plain_r<T, 3>(b, tall, sms, s);
-        default: return launch_plain_r<T, 4>(b, tall, sms, s);
+        case 1: return launch_plain_r<T, 1>(b, rows, sms, s);
+        case 2: return launch_plain_r<T, 2>(b, rows, sms, s);
+        case 3: return launch_plain_r<T, 3>(b, rows, sms, s);
+        default: return launch_plain_r<T, 4>(b, rows, sms, s);
     }
 }
 
