@@ -38,9 +38,10 @@ constexpr int kPlainCost = 2;   // a unit's own cost, in key tiles
 template <typename T, int kC, int kR, int kS>
 struct Plain {
     static constexpr int kRows = 16 / kS * kR;
-    static constexpr int kKeys = kC == 1 ? 64 : 32;
+    static constexpr int kKeys = kC == 1 || kS == 4 ? 64 : 32;
     static constexpr int kPad = 16 / (int)sizeof(T);
-    static_assert(kS == 1 || (kKeys % (16 * kS) == 0 && 4 * kS * kRows <= 2 * kKeys * (int)sizeof(T)), "the shares' sums fit where the keys were");
+    static_assert(kS == 1 || (kKeys % (16 * kS) == 0 && kS * kRows <= kKeys * (int)sizeof(T) && kS * kRows <= 8 * kKeys),
+                  "the shares' sums fit where the tiles were, their maxima in the rows' padding");
     static size_t smem(int D) {
         return 4 * (size_t)kKeys * (D + kPad) * sizeof(T) + (size_t)kRows * (D + 4) * 4 + (size_t)kRows * (kKeys + 4) * 4 +
                2 * kKeys * sizeof(long long) + sizeof(LineStart);
@@ -55,8 +56,22 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// Sixteen bytes of a row.
+template <typename T>
+struct Word {
+    uint32_t u[4];
+    __device__ __forceinline__ void load(const T* p) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(u[i & 3]);
+        return __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
+    }
+};
+
 template <typename T, int kC, int kR, int kS>
-__global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(256, kR * kC >= 16 ? 1 : 2) attention_plain_kernel(const AttentionArgs a) {
     using P = Plain<T, kC, kR, kS>;
     using Walk = LineWalk<P::kRows, P::kKeys, kPlainCost>;
     constexpr int kRows = P::kRows, kKeys = P::kKeys, kShare = kKeys / kS, kJ = kShare / 16;
@@ -80,12 +95,15 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
     for (bool more = W.start(a, S); more; more = W.next(a)) {
         const int n = W.q.n, ctx = W.q.ctx, len = ctx + n, nrows = W.rows(a), r0 = W.rt * kRows;
         const int32_t* table = a.page_table + (size_t)W.r * a.max_pages;
-        auto locate = [&](int j) {   // the places of tile j's rows
+        auto look = [&](int j) {   // the page of this thread's row of tile j; -2: no row
+            const int pos = (W.kt + j) * kKeys + tid;
+            return tid < kKeys && pos < len ? table[pos / a.page_size] : -2;
+        };
+        auto locate = [&](int j, int id) {   // the places of tile j's rows
             if (tid < kKeys) {
                 const int pos = (W.kt + j) * kKeys + tid;
                 long long at = -1;
-                if (pos < len) {
-                    const int id = table[pos / a.page_size];
+                if (id != -2) {
                     if (id < 0 || id >= a.n_pages) raise_flag(a.flags, kFlagBadIndex);
                     else at = (((long long)id * a.kv_heads + W.h) * a.page_size + pos % a.page_size) * D;
                 }
@@ -106,7 +124,8 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        locate(0);
+        locate(0, look(0));
+        if (W.nk > 1) locate(1, look(1));
         for (int x = tid; x < kRows * (D / 4); x += 256) {
             const int row = x / (D / 4), ch = x - row * (D / 4), gr = r0 + row;
             float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -128,10 +147,11 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
                 for (int z = 0; z < 4; ++z) o[i][y][z] = 0.f;
         }
         for (int j = 0; j < W.nk; ++j) {
-            if (j + 1 < W.nk) locate(j + 1);
             __syncthreads();
+            int id = -2;   // the page of the tile after next is on its way during this tile
             if (j + 1 < W.nk) {
                 fetch(j + 1);
+                if (j + 2 < W.nk) id = look(j + 2);
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -145,17 +165,19 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
                 for (int y = 0; y < kJ; ++y) s[i][y] = 0.f;
             const T* kt = ks + ((size_t)(j & 1) * kKeys + key0) * ld;
 #pragma unroll 2
-            for (int d = 0; d < D; d += 4) {
-                float4 k[kJ];
+            for (int d = 0; d < D; d += P::kPad) {
+                Word<T> k[kJ];
 #pragma unroll
-                for (int y = 0; y < kJ; ++y) k[y] = load4(kt + (tx + 16 * y) * ld + d);
+                for (int y = 0; y < kJ; ++y) k[y].load(kt + (tx + 16 * y) * ld + d);
 #pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    const float4 q = *reinterpret_cast<const float4*>(qs + (ty * kR + i) * (D + 4) + d);
+                for (int i = 0; i < kR; ++i)
 #pragma unroll
-                    for (int y = 0; y < kJ; ++y)
-                        s[i][y] = fmaf(q.x, k[y].x, fmaf(q.y, k[y].y, fmaf(q.z, k[y].z, fmaf(q.w, k[y].w, s[i][y]))));
-                }
+                    for (int z = 0; z < P::kPad; z += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(qs + (ty * kR + i) * (D + 4) + d + z);
+#pragma unroll
+                        for (int y = 0; y < kJ; ++y)
+                            s[i][y] = fmaf(q.x, k[y].at(z), fmaf(q.y, k[y].at(z + 1), fmaf(q.z, k[y].at(z + 2), fmaf(q.w, k[y].at(z + 3), s[i][y]))));
+                    }
             }
             const int k0 = (W.kt + j) * kKeys;
             const bool masked = k0 + kKeys > ctx;
@@ -227,6 +249,7 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
             };
             if (masked) product(std::true_type{});
             else product(std::false_type{});
+            if (j + 2 < W.nk) locate(j + 2, id);
         }
         // ---- the unit's result, or its part ----
         const bool whole = W.nk == W.q.nkt;
@@ -255,10 +278,10 @@ __global__ void __launch_bounds__(256) attention_plain_kernel(const AttentionArg
                     if (tx * 4 + 64 * y < D) put(row, tx + 16 * y, make_float4(o[i][y][0], o[i][y][1], o[i][y][2], o[i][y][3]), m[i], l[i]);
             }
         } else {
-            // the shares' sums meet where the keys were: [kS][kRows][D], and
-            // their maxima and sums [kS][kRows] where the values were
+            // the shares' sums meet where the tiles were: [kS][kRows][D], and
+            // behind them their maxima and sums of weights [kS][kRows]
             float* os = reinterpret_cast<float*>(ks);
-            float2* mls = reinterpret_cast<float2*>(vs);
+            float2* mls = reinterpret_cast<float2*>(os + kS * kRows * D);
             const int z = key0 / kShare;
             __syncthreads();   // the last tile's keys and values have been read
 #pragma unroll
@@ -327,18 +350,26 @@ cudaError_t launch_plain_t(const AttentionArgs& a, int sms, cudaStream_t s) {
 
 template <typename T, int kC>
 cudaError_t launch_plain_r(const AttentionArgs& a, int rows, int sms, cudaStream_t s) {
-    constexpr int kS = kC == 1 ? 4 : 2;   // shares of 16 keys
+    // What bounds units of few rows is the tiles' way from shared memory to the
+    // registers: with shares a key serves the unit's rows in fewer warps.  Four
+    // shares need tiles of 64 keys, of which two blocks an SM fit up to 4 bytes x
+    // 64 components; beyond, two shares, except for up to 4 rows.  64 tokens at up
+    // to 4000 positions, one / two / four shares: fp32, 8 rows of 64 components
+    // 94.6 / - / 50.6 us, of 128 165 / 107 / 147 (one block an SM), one row of 128
+    // 315 / 201 / 167; bf16, 8 rows of 128, pages of 1 373 / 242 / 150.  32 rows in
+    // shares (8 a thread) were no faster: 16 trees of 40 79 against 81 us.
+    constexpr int kS = kC * sizeof(T) <= 4 ? 4 : 2;
     if (rows > 32) return launch_plain_t<T, kC, 4, 1>(a, sms, s);
     if (rows > 16) return launch_plain_t<T, kC, 2, 1>(a, sms, s);
     if (rows > 8) return launch_plain_t<T, kC, kS, kS>(a, sms, s);
-    if (rows > 4 || kS == 2) return launch_plain_t<T, kC, kS / 2, kS>(a, sms, s);
-    return launch_plain_t<T, kC, 1, kS>(a, sms, s);
+    if (rows > 4 || kC * sizeof(T) > 8) return launch_plain_t<T, kC, kS / 2, kS>(a, sms, s);
+    return launch_plain_t<T, kC, 1, (kC * sizeof(T) > 8 ? kS : 4)>(a, sms, s);
 }
 
 template <typename T>
 cudaError_t launch_plain(const AttentionArgs& a, int sms, cudaStream_t s) {
     if (sms <= 0) return cudaErrorNotSupported;
-    // Units of 16, 32 or 64 rows, by the requests' rows a key head on average.
+    // Units of 4 to 64 rows, by the requests' rows a key head on average.
     AttentionArgs b = a;
     const long long mean = ((long long)a.T * a.group + a.R - 1) / a.R;
     b.min_steps = 1;
