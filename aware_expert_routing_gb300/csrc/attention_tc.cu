@@ -59,9 +59,11 @@ namespace {
 constexpr int kKeys = 128;     // keys per tile
 constexpr int kRowsTile = 128; // query rows per tile
 constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O from here
-// See attention_line.cuh.  16 trees of 16 to 4000, all of it before the tiles
-// and with an earlier softmax: 2: 32.7, 3: 31.9, 4: 30.6, 5: 29.4, 6: 29.5 us.
-constexpr int kUnitCost = 5;
+// See attention_line.cuh.  3 / 4 / 5: 16 trees of 16 to 4000 25.3 / 24.4 / 24.4 us
+// (replayed from a graph), 96 pairs of tokens at 127 16.6 / 16.5 / 18.1, 64 tokens
+// to 8000 87.7 / 88.3 / 89.0, 38 trees of 12 to 7666 54.1 / 54.7 / 56.4, one token
+// at 1000 9.6 / 9.6 / 9.4; 6 and 8 were no better.
+constexpr int kUnitCost = 4;
 constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
 
 // Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
