@@ -11,10 +11,10 @@
 // the cache's bytes bound the kernel while a key head has fewer than about
 // 250 rows, and the chain from S over the softmax to P V above.  Measured, with
 // heads of 128 and 4 key heads: 256 single tokens up to 16000 positions (4.53
-// GB) 663 us, 6.8 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 90 us,
-// 5.9 TB/s, its DRAM reads 1.00 of these bytes; a tree of 64 tokens with 8 query
+// GB) 650 us, 7.0 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 88 us,
+// 6.0 TB/s, its DRAM reads 1.00 of these bytes; a tree of 64 tokens with 8 query
 // heads a key head at 131000 positions 117 us, 1.17 PFLOP/s; one token at 1000
-// positions 9.4 us, nearly all of it latency: lengths, table, tile, S, P, O and
+// positions 10 us, nearly all of it latency: lengths, table, tile, S, P, O and
 // the join one after the other.
 //
 //   * Work.  A unit is (request, key head, tile of rows); its key tiles follow
@@ -35,7 +35,18 @@
 //     128 rows) the next tile's S is computed while the softmax works on this
 //     one; with two (up to 256 rows) each has a buffer and they take turns, and
 //     each tile of keys and values is read once for both.
-//   * P replaces S in tensor memory (bf16) and is the A operand of P V.
+//   * Units of few rows would leave most of a tile's 128 rows empty and one warp
+//     with all exponentials.  There the tile holds the unit's rows four times
+//     (up to 16 rows) or twice (up to 64): each copy, or share, has a quarter or
+//     half of the keys, its own maximum and sum, P zero elsewhere and its own O,
+//     and the shares meet at the unit's end.
+//   * P replaces S in tensor memory and is the A operand of P V, in bf16.  With
+//     shares it is two bf16 numbers (the weight and what rounding left of it),
+//     since with few rows one rounded large weight shows: the result's error is
+//     then that of its own rounding alone.  Without shares it is one, which puts
+//     the error of some hundred rows at 1.2 to 1.3 times that (two would be 1.00,
+//     but 31 against 24 us for 16 trees of 16 to 4000, 149 against 112 for a tree
+//     of 64 at 131000).
 //   * O is corrected only when a row's maximum has grown by more than 8 powers
 //     of two since the last correction (P then stays below 2^8, exact in the
 //     sums), so almost never after the first tiles.
@@ -101,6 +112,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
+        : "memory");
+}
+
+// Two weights as bf16, and what that leaves of them as bf16 again.
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& low) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+    hi = *reinterpret_cast<const uint32_t*>(&p);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+    low = *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Two components of a result, over the row's sum l (its inverse inv); 0 for an empty row.
+__device__ __forceinline__ uint32_t round2(float x, float y, float l, float inv) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(l == 0.f ? 0.f : x * inv, l == 0.f ? 0.f : y * inv);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+        "};"
+        ::"r"(taddr),
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -176,7 +212,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, int kShares>
 struct Cfg {
     // warps 0 and 1 copy and issue MMAs, the softmax's warpgroups follow; two
     // of those start at a warpgroup's boundary, so that registers can be moved
@@ -188,8 +224,14 @@ struct Cfg {
     static constexpr int kQTile = kRowsTile * D * 2;
     static constexpr int kControl = 2048;
     static constexpr int kSmem = 227 * 1024;
-    static constexpr int kStages = (kSmem - 1024 - kControl - kTiles * kQTile) / kStage;
-    static constexpr int kRows = kRowsTile * kTiles;    // rows of a unit
+    static constexpr int kSpan = kRowsTile / kShares;   // rows of a tile that a share has
+    static constexpr int kRows = kShares == 4 ? 16 : kSpan * kTiles;   // rows of a unit
+    // Where shares meet: as many blocks of 32 components at once as there are shares.
+    static constexpr int kAtOnce = D / 32 < kShares ? D / 32 : kShares;
+    static constexpr int kMeet = kAtOnce * (kShares - 1) * kRows * 128;
+    static constexpr int kStages = (kSmem - 1024 - kControl - kTiles * kQTile - kMeet) / kStage;
+    static constexpr bool kLow = kShares > 1;
+    static_assert(kStages <= 16 && (kTiles == 1 || kShares == 1), "barriers; shares of one row tile");
 };
 
 struct Control {
@@ -198,6 +240,7 @@ struct Control {
     LineStart start;
     int abort_flag;
     uint32_t tmem_base;
+    float2 ml[kRowsTile];      // shares' maxima and sums, when they meet
     uint32_t bad[2][2][4];     // per row tile and key tile's parity: keys whose value is not finite
 };
 static_assert(sizeof(Control) <= 2048, "control block");
@@ -244,16 +287,16 @@ __device__ __forceinline__ void seen_bits(const uint32_t* mrow, int words, uint3
     for (int x = 0; x < 4; ++x) bits[x] = __funnelshift_r(v[x], v[x + 1], d0 & 31);
 }
 
-template <int D, int kTiles>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
+template <int D, int kTiles, int kShares>
+__global__ void __launch_bounds__(Cfg<D, kTiles, kShares>::kThreads, 1)
 attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-    using C = Cfg<D, kTiles>;
+    using C = Cfg<D, kTiles, kShares>;
     using Walk = LineWalk<C::kRows, kKeys, kUnitCost>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* ring = smem;                                 // [kStages][kStage]
     unsigned char* qs = smem + C::kStages * C::kStage;          // [kTiles][kQTile]
-    Control& S = *reinterpret_cast<Control*>(qs + kTiles * C::kQTile);
+    Control& S = *reinterpret_cast<Control*>(qs + kTiles * C::kQTile + C::kMeet);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.group;
     // rows of row tile w of a unit
@@ -405,7 +448,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     wait_bar(&S.p_full[buf], pp, S, a.flags);
                     tmem_fence_after_sync();
                 }
-                mma_ts(d, p + k * 8, v_hi | (va + k * 2 * C::kBlocks * 1024 / 16), idesc_o, k > 0 ? 1u : acc);
+                const uint32_t pk = p + (k / 4) * 64 + (k % 4) * 8;
+                const uint64_t vk = v_hi | (va + k * 2 * C::kBlocks * 1024 / 16);
+                mma_ts(d, pk, vk, idesc_o, k > 0 ? 1u : acc);
+                if (C::kLow) mma_ts(d, pk + 32, vk, idesc_o, 1u);
             }
             mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
         };
@@ -473,7 +519,11 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         // registers: 384 x 168 at launch = 128 x 120 + 256 x 192
         if (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int w = (warp - C::kFirst) >> 2, quad = warp & 3;
-        const int row = quad * 32 + lane;
+        // With shares, each holds the unit's rows again, for its own keys of a tile.
+        constexpr int kWarps = 4 / kShares;           // of a share
+        const int share = kShares == 1 ? 0 : quad / kWarps;
+        const int row = kShares == 1 ? quad * 32 + lane : quad % kWarps * 32 + lane;
+        const int krow = quad * 32 + lane;            // the key of a tile that this thread looks after
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const int qwarp = (warp - C::kFirst) & 3;     // this warp's share of the query copy
         unsigned char* q_dst = qs + w * C::kQTile;
@@ -507,7 +557,9 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             static_assert(kStep % 8 == 0, "the swizzle is the same at every step");
 #pragma unroll 4
             for (int r0 = qrow; r0 < rows; r0 += kStep) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+#pragma unroll
+                for (int x = 0; x < kShares; ++x)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + x * C::kSpan * 128), "l"(src) : "memory");
                 to += kStep * 128;
                 src += step;
                 g += step_g;
@@ -558,7 +610,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 }
                 continue;
             }
-            const bool live = quad * 32 < nr;          // this warp has rows
+            const bool live = row - lane < nr;         // this warp has rows
             const bool valid = row < nr;
             const int gr = U.rt * C::kRows + w * kRowsTile + (valid ? row : 0);
             const int ti = gr / group;                 // token within the request
@@ -584,34 +636,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     copy_q(W, rows);
                     read_mask(W, rows);
                 }
-                // The maximum, then P, 64 columns at a time.  With one row
-                // tile the row stays in registers between the two; with two
-                // (192 registers) it would spill, and S is read twice: 117
-                // against 121 us for 1x64 at 131000.  (One tile: 27.6
-                // against 28.4 us for 16 trees of 16 to 4000.)
-                constexpr bool kHold = kTiles == 1;
-                constexpr int kTimes = kHold ? 2 : 1;
-                uint32_t s[kTimes][64];
-                auto load_s = [&](int x) {
-                    uint32_t(&h)[64] = s[kHold ? x : 0];
-                    tmem_ld64(lanes + buf * 128 + x * 64, h);
-                    if (masked) {
-                        const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
-#pragma unroll
-                        for (int y = 0; y < 64; ++y)
-                            if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) h[y] = 0xff800000u;   // -inf
-                    }
-                };
-                float off = 0.f;
-                if (live) {
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll kTimes
-                    for (int x = 0; x < 2; ++x) {
-                        load_s(x);
-#pragma unroll
-                        for (int y = 0; y < 64; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[kHold ? x : 0][y]));
-                    }
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                constexpr int kWidth = kKeys / kShares;   // a share's keys of a tile
+                uint32_t own32[32], own64[64];
+                // m for a tile of maximum mt; returns the exponents' offset.
+                auto new_max = [&](float mt) {
                     if (j == 0) {
                         m = mt;
                     } else {
@@ -634,19 +662,64 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             m = mn;
                         }
                     }
-                    off = m == -INFINITY ? 0.f : -m * c;
+                    return m == -INFINITY ? 0.f : -m * c;
+                };
+                // The maximum, then P, 64 columns at a time.  With one row
+                // tile the row stays in registers between the two; with two
+                // (192 registers) it would spill, and S is read twice: 117
+                // against 121 us for 1x64 at 131000.  (One tile: 27.6
+                // against 28.4 us for 16 trees of 16 to 4000.)
+                constexpr bool kHold = kTiles == 1;
+                constexpr int kTimes = kHold ? 2 : 1;
+                uint32_t s[kTimes][64];
+                auto load_s = [&](int x) {
+                    uint32_t(&h)[64] = s[kHold ? x : 0];
+                    tmem_ld64(lanes + buf * 128 + x * 64, h);
+                    if (masked) {
+                        const uint32_t b0 = x ? bits[2] : bits[0], b1 = x ? bits[3] : bits[1];
+#pragma unroll
+                        for (int y = 0; y < 64; ++y)
+                            if (!(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) h[y] = 0xff800000u;   // -inf
+                    }
+                };
+                float off = 0.f;
+                if (kShares > 1) {
+                    if (live) {
+                        if (kWidth == 32) tmem_ld32(lanes + buf * 128 + share * 32, own32);
+                        else tmem_ld64(lanes + buf * 128 + share * 64, own64);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        const uint32_t b0 = kWidth == 64 ? (share ? bits[2] : bits[0]) : share < 2 ? (share ? bits[1] : bits[0]) : share == 2 ? bits[2] : bits[3];
+                        const uint32_t b1 = share ? bits[3] : bits[1];
+#pragma unroll
+                        for (int y = 0; y < kWidth; ++y) {
+                            uint32_t& v = kWidth == 32 ? own32[y & 31] : own64[y];
+                            if (masked && !(((y < 32 ? b0 : b1) >> (y & 31)) & 1u)) v = 0xff800000u;   // -inf
+                            mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(v));
+                        }
+                        off = new_max(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    }
+                } else if (live) {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll kTimes
+                    for (int x = 0; x < 2; ++x) {
+                        load_s(x);
+#pragma unroll
+                        for (int y = 0; y < 64; ++y) mx[y & 3] = fmaxf(mx[y & 3], __uint_as_float(s[kHold ? x : 0][y]));
+                    }
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    off = new_max(mt);
                 }
                 if (masked) {
                     // value rows past the context: zero those past the length, and those that are not finite
                     const uint32_t vseq = seq + (kTiles == 2 ? 2 * j + 1 : j == U.nk - 1 ? 2 * j + 1 : 2 * j + 2);
                     wait_bar(&S.full[vseq % C::kStages], (vseq / C::kStages) & 1, S, a.flags);
-                    unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (row >> 3) * (C::kBlocks * 1024) + (row & 7) * 128;
+                    unsigned char* vrow = ring + (vseq % C::kStages) * C::kStage + (krow >> 3) * (C::kBlocks * 1024) + (krow & 7) * 128;
                     // (a bf16 of all-ones exponent carries into bit 15 when 0x80 is added)
                     uint32_t top = 0;
-                    if (k0 + row >= U.q.ctx && k0 + row < len)
+                    if (k0 + krow >= U.q.ctx && k0 + krow < len)
 #pragma unroll 4
                         for (int x = 0; x < D / 8; ++x) {   // the swizzle's order: no two rows of eight in one bank
-                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4));
+                            const uint4 v = *reinterpret_cast<const uint4*>(vrow + (x >> 3) * 1024 + (((x ^ krow) & 7) << 4));
                             top |= ((v.x & 0x7fff7fffu) + 0x00800080u) | ((v.y & 0x7fff7fffu) + 0x00800080u) |
                                    ((v.z & 0x7fff7fffu) + 0x00800080u) | ((v.w & 0x7fff7fffu) + 0x00800080u);
                         }
@@ -655,16 +728,60 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                     if (lane == 0) S.bad[w][tile & 1][quad] = badw;   // the other parity may still be read
                     // all have looked before anyone zeroes
                     if (both) named_barrier(1, 256); else named_barrier(2 + w, 128);
-                    if (w == 0 && (bad || k0 + row >= len))
+                    if (w == 0 && (bad || k0 + krow >= len))
 #pragma unroll 4
                         for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (((x ^ row) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vrow + (x >> 3) * 1024 + (((x ^ krow) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     if (w == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         if (bits[x] & S.bad[w][tile & 1][x]) poison = NAN;
                 }
-                if (live) {
+                if (kShares > 1) {
+                    // P of this share's keys, in two bf16 parts; zero where the other shares' keys are
+                    if (live) {
+                        const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
+                        uint64_t sum[2] = {0, 0};
+                        uint32_t hi[32], low[32], none[32];
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) none[y] = 0;
+#pragma unroll
+                        for (int y = 0; y < kWidth / 2; ++y) {
+                            float p0, p1;
+                            unpack2(fma2(pack2(__uint_as_float(kWidth == 32 ? own32[(2 * y) & 31] : own64[2 * y]),
+                                               __uint_as_float(kWidth == 32 ? own32[(2 * y + 1) & 31] : own64[2 * y + 1])), c2, off2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+                            split2(p0, p1, hi[y], low[y]);
+                        }
+                        const uint32_t at = lanes + buf * 128;
+                        if (kWidth == 32) {
+                            const uint32_t mine = at + (share >> 1) * 64 + (share & 1) * 16, other = at + (share >> 1) * 64 + (~share & 1) * 16;
+                            tmem_st16(mine, hi);
+                            tmem_st16(mine + 32, low);
+                            tmem_st16(other, none);
+                            tmem_st16(other + 32, none);
+                            tmem_st32(at + (~share >> 1 & 1) * 64, none);
+                            tmem_st32(at + (~share >> 1 & 1) * 64 + 32, none);
+                        } else {
+                            tmem_st32(at + share * 64, hi);
+                            tmem_st32(at + share * 64 + 32, low);
+                            tmem_st32(at + (share ^ 1) * 64, none);
+                            tmem_st32(at + (share ^ 1) * 64 + 32, none);
+                        }
+                        tmem_wait_st();
+                        float s0, s1;
+                        unpack2(add2(sum[0], sum[1]), s0, s1);
+                        l += s0 + s1 + poison;
+                    }
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&S.p_half[buf]);
+                        mbar_arrive(&S.p_full[buf]);
+                    }
+                } else if (live) {
                     const uint64_t c2 = pack2(c, c), off2 = pack2(off, off);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll kTimes
@@ -681,7 +798,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                             const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
                             h[y] = *reinterpret_cast<const uint32_t*>(&p);
                         }
-                        tmem_st32(lanes + buf * 128 + x * 32, h);   // over columns of S that have been read
+                        tmem_st32(lanes + buf * 128 + x * 64, h);   // over columns of S that have been read
                         tmem_wait_st();
                         tmem_fence_before_sync();
                         __syncwarp();
@@ -705,7 +822,74 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             // ---- the unit's result, or its part ----
             wait_pv(tile - 1);
             tmem_fence_after_sync();
-            if (live) {
+            if (kShares > 1) {
+                // the shares meet, 32 components at a time, each time with another of them
+                S.ml[krow] = make_float2(m, l);
+                named_barrier(2, 128);
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int x = 0; x < kShares; ++x) M = fmaxf(M, S.ml[x * C::kSpan + row].x);
+#pragma unroll
+                for (int x = 0; x < kShares; ++x) {
+                    const float2 e = S.ml[x * C::kSpan + row];
+                    L = fmaf(e.x == -INFINITY ? 0.f : ex2((e.x - M) * c), e.y, L);
+                }
+                const float f = m == -INFINITY ? 0.f : ex2((m - M) * c), inv = L == 0.f ? 0.f : 1.f / L;
+                float4* meet = reinterpret_cast<float4*>(qs + kTiles * C::kQTile) + row;
+                float4 v[8];
+                auto load_o = [&](int x) {
+                    uint32_t o[32];
+                    __syncwarp();   // the load is the whole warp's
+                    tmem_ld32(lanes + kOCol + x * 32, o);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        v[y] = make_float4(__uint_as_float(o[4 * y]) * f, __uint_as_float(o[4 * y + 1]) * f,
+                                           __uint_as_float(o[4 * y + 2]) * f, __uint_as_float(o[4 * y + 3]) * f);
+                };
+#pragma unroll 1
+                for (int x0 = 0; x0 < D / 32; x0 += C::kAtOnce) {
+                    __syncwarp();
+                    if (x0 > 0) named_barrier(2, 128);   // the last ones have been read
+#pragma unroll 1
+                    for (int x = 0; x < C::kAtOnce; ++x) {
+                        if (x == share) continue;
+                        load_o(x0 + x);
+                        if (valid)
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                meet[((x * (kShares - 1) + (share < x ? share : share - 1)) * 8 + y) * C::kRows] = v[y];
+                    }
+                    named_barrier(2, 128);
+                    if (share >= C::kAtOnce) continue;
+                    const int x = x0 + share;
+                    load_o(x);
+                    if (!valid) continue;
+#pragma unroll
+                    for (int z = 0; z < kShares - 1; ++z)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float4 e = meet[((share * (kShares - 1) + z) * 8 + y) * C::kRows];
+                            v[y] = make_float4(v[y].x + e.x, v[y].y + e.y, v[y].z + e.z, v[y].w + e.w);
+                        }
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + x * 32);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            dst[y] = make_uint4(round2(v[2 * y].x, v[2 * y].y, L, inv), round2(v[2 * y].z, v[2 * y].w, L, inv),
+                                                round2(v[2 * y + 1].x, v[2 * y + 1].y, L, inv), round2(v[2 * y + 1].z, v[2 * y + 1].w, L, inv));
+                    } else {
+                        float4* part = reinterpret_cast<float4*>(a.o) + ((size_t)slot * a.rows + (row - lane)) * (D / 4) + lane;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) part[(x * 8 + y) * 32] = v[y];
+                    }
+                }
+                __syncwarp();
+                if (valid && share == 0) {
+                    if (!whole) a.ml[(size_t)slot * a.rows + row] = make_float2(M * c, L);
+                    else if (a.lse) a.lse[orow] = L == 0.f ? -INFINITY : M * a.scale + logf(L);
+                }
+                tmem_fence_before_sync();   // read before the next unit's product overwrites O
+            } else if (live) {
                 const size_t prow = (size_t)slot * a.rows + w * kRowsTile + row;
                 // 32 rows of a part lie side by side: [D / 4][32] float4
                 float4* part = reinterpret_cast<float4*>(a.o) + ((size_t)slot * a.rows + w * kRowsTile + quad * 32) * (D / 4) + lane;
@@ -768,16 +952,16 @@ bool encode_cache(CUtensorMap* m, PFN_cuTensorMapEncodeTiled_v12000 enc, const v
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, int kShares>
 cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t s) {
-    using C = Cfg<D, kTiles>;
+    using C = Cfg<D, kTiles, kShares>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(attention_tc_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(attention_tc_kernel<D, kTiles, kShares>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
@@ -791,7 +975,7 @@ cudaError_t launch_t(const AttentionArgs& a, const CUtensorMap& mk, const CUtens
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<D, kTiles>, a, mk, mv);
+    e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<D, kTiles, kShares>, a, mk, mv);
     if (e != cudaSuccess) return e;
     // a unit of one key tile is never cut
     if ((long long)a.max_pages * a.page_size <= kKeys || grid < 2) return cudaSuccess;
@@ -817,8 +1001,18 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s)
     // 20.2, 4 21.8, 6 23.5 us; of up to 128 rows no difference).
     AttentionArgs b = a;
     b.min_steps = two ? 2 : 1;
-    if (a.D == 128) return two ? launch_t<128, 2>(b, mk, mv, grid, s) : launch_t<128, 1>(b, mk, mv, grid, s);
-    return two ? launch_t<64, 2>(b, mk, mv, grid, s) : launch_t<64, 1>(b, mk, mv, grid, s);
+    // Shares by the requests' rows a key head on average, with room for those
+    // above it, or by the one token that each has.  No shares and P in one bf16 /
+    // in two / shares and two: 64 tokens to 8000 89.2 / 121.0 / 88.4 us, 256 to
+    // 16000 671 / 851 / 642, 15 to 5778 16.0 / 18.5 / 14.7, one at 1000 9.6 / 10.2
+    // / 10.1, 38 trees of 12 with 4 heads a key head 55.2 / 70.3 / 55.8.
+    const long long all = (long long)a.T * a.group;
+    const int shares = all <= 12LL * a.R || (a.T <= a.R && a.group <= 16) ? 4 : all <= 48LL * a.R || (a.T <= a.R && a.group <= 64) ? 2 : 1;
+    if (a.D == 128)
+        return two ? launch_t<128, 2, 1>(b, mk, mv, grid, s) : shares == 4 ? launch_t<128, 1, 4>(b, mk, mv, grid, s)
+                   : shares == 2 ? launch_t<128, 1, 2>(b, mk, mv, grid, s) : launch_t<128, 1, 1>(b, mk, mv, grid, s);
+    return two ? launch_t<64, 2, 1>(b, mk, mv, grid, s) : shares == 4 ? launch_t<64, 1, 4>(b, mk, mv, grid, s)
+               : shares == 2 ? launch_t<64, 1, 2>(b, mk, mv, grid, s) : launch_t<64, 1, 1>(b, mk, mv, grid, s);
 }
 
 }  // namespace moe

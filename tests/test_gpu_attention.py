@@ -344,3 +344,85 @@ def test_many_requests(R, most, n, H, K, D, page, dtype):
     for _ in range(5):
         out2, l2, _ = c.run()
         assert torch.equal(out, out2) and torch.equal(l, l2)
+
+
+# The same questions at other numbers of rows a key head: few rows share out a tile's keys, many share its copies.
+@pytest.mark.parametrize("H", [4, 32, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_unseen_positions_have_no_influence_at_any_number_of_rows(H, D, bad):
+    ctx, n = [300, 0, 127], [5, 3, 1]
+    c = Case(ctx, n, H, 2, D, 16, "bf16", True, 41)
+    c.mask[:, 0] &= ~4
+    seen = torch.zeros(c.k.shape[0], 16, dtype=torch.bool)
+    for r in range(3):
+        for j in range(ctx[r] + n[r]):
+            if j != ctx[r] + 2:
+                seen[c.table[r, j // 16].long(), j % 16] = True
+    c.k.permute(0, 2, 1, 3)[~seen] = bad
+    c.v.permute(0, 2, 1, 3)[~seen] = bad
+    out, l, flags = c.run()
+    assert flags == 0
+    c.k.permute(0, 2, 1, 3)[~seen] = 0.0
+    c.v.permute(0, 2, 1, 3)[~seen] = 0.0
+    c.check(out, l)
+
+
+@pytest.mark.parametrize("H", [4, 32, 64])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_a_siblings_nan_at_any_number_of_rows(H, what):
+    c = Case([150], [6], H, 2, 128, 16, "bf16", True, 42)
+    c.mask[:, 0] = torch.tensor([1, 3, 5, 7, 17, 33], dtype=torch.int32)
+    x = getattr(c, what)
+    x[c.table[0, 152 // 16].long(), :, 152 % 16, 5] = float("nan")
+    out, l, flags = c.run()
+    assert flags == 0
+    spoilt = out.cpu().isnan().flatten(1).any(1)
+    assert spoilt.tolist() == [False, False, True, True, False, False]
+    x.nan_to_num_(0.0)
+    o, e, to, te = ref.attend(c.q, c.k, c.v, c.table, c.off, c.ctx, c.mask, c.scale, True)
+    assert ((out.cpu().double() - o).abs() <= to)[~spoilt].all()
+
+
+@pytest.mark.parametrize("H", [4, 32, 64, 160])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["rising", "falling", "one far above", "very negative"])
+def test_running_maximum_at_any_number_of_rows(H, D, kind):
+    c = Case([900], [2], H, 2, D, 16, "bf16", False, 43, q_scale=0.0)
+    c.q[..., 0] = 11.3 * (D / 128) ** 0.5
+    j = torch.arange(902)
+    s = {"rising": j * 0.11, "falling": -j * 0.11, "one far above": (j == 701) * 60.0, "very negative": -300.0 - j * 0.05}[kind]
+    k = c.k.float()
+    k[c.table[0].long()[j // 16], :, j % 16, 0] = s.float()[:, None]
+    c.k = k.to(c.dt)
+    out, l, flags = c.run()
+    assert flags == 0
+    c.check(out, l)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("singles,many", [(29, 13), (19, 13), (3, 40), (1, 70)])
+def test_many_tokens_of_one_request_among_single_ones(singles, many, D):
+    """The units' height follows the mean: the request with many tokens has several units, or all fill a part of one."""
+    g = torch.Generator().manual_seed(44)
+    ctx = torch.randint(0, 700, (singles + 1,), generator=g).tolist()
+    n = [1] * singles + [many]
+    c = Case(ctx, n, 16, 2, D, 16, "bf16", True, 45)
+    out, l, flags = c.run()
+    assert flags == 0
+    c.check(out, l)
+    again, l2, _ = c.run()
+    assert torch.equal(again, out) and torch.equal(l2, l)
+
+
+@pytest.mark.parametrize("ctx,n,H", [(500, 1, 2), (1000, 1, 2), (3000, 1, 32), (3000, 2, 40), (700, 3, 32)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_lose_nothing_but_the_results_rounding(ctx, n, H, D):
+    """With few rows a key head (up to 48 on average) a weight enters the product as two bf16 numbers, good to 2^-16 of
+    it, against 2^-9 of the result's own rounding: the error is the rounding's, within a hundredth (2^-16 / 2^-9 = 1/128)."""
+    for seed in range(5):
+        c = Case([ctx], [n], H, 2, D, 16, "bf16", False, 50 + seed)
+        out, _, flags = c.run()
+        assert flags == 0
+        o = ref.attend(c.q, c.k, c.v, c.table, c.off, c.ctx, c.mask, c.scale, True)[0]
+        assert (out.cpu().double() - o).norm() <= 1.01 * (o.bfloat16().double() - o).norm()
