@@ -1007,7 +1007,10 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s)
     // 16000 671 / 851 / 642, 15 to 5778 16.0 / 18.5 / 14.7, one at 1000 9.6 / 10.2
     // / 10.1, 38 trees of 12 with 4 heads a key head 55.2 / 70.3 / 55.8.
     const long long all = (long long)a.T * a.group;
-    const int shares = all <= 12LL * a.R || (a.T <= a.R && a.group <= 16) ? 4 : all <= 48LL * a.R || (a.T <= a.R && a.group <= 64) ? 2 : 1;
+    const bool even = a.R == 1;   // the mean is all there is
+    const int shares = all <= (even ? 16 : 12) * (long long)a.R || (a.T <= a.R && a.group <= 16)   ? 4
+                       : all <= (even ? 64 : 48) * (long long)a.R || (a.T <= a.R && a.group <= 64) ? 2
+                                                                                                   : 1;
     if (a.D == 128)
         return two ? launch_t<128, 2, 1>(b, mk, mv, grid, s) : shares == 4 ? launch_t<128, 1, 4>(b, mk, mv, grid, s)
                    : shares == 2 ? launch_t<128, 1, 2>(b, mk, mv, grid, s) : launch_t<128, 1, 1>(b, mk, mv, grid, s);
