@@ -11,7 +11,7 @@
 // other sizes.  fp32 has no tensor-core path that keeps fp32's accuracy, so its
 // bound is the FMA rate (74 TFLOP/s at 1.9 GHz) from about 11 query rows a key
 // head on, and the cache's bytes below.  Measured, 4 trees of 7 tokens up to
-// 2000 positions, 8 + 2 heads of 64: 15.0 us, of which the bytes would take 0.6;
+// 2000 positions, 8 + 2 heads of 64: 14.6 us, of which the bytes would take 0.6;
 // at this length the steps of one unit (lengths, table, tile, scores, softmax,
 // values) wait for one another.
 #include <type_traits>

@@ -11,7 +11,7 @@
 // the cache's bytes bound the kernel while a key head has fewer than about
 // 250 rows, and the chain from S over the softmax to P V above.  Measured, with
 // heads of 128 and 4 key heads: 256 single tokens up to 16000 positions (4.53
-// GB) 650 us, 7.0 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 88 us,
+// GB) 665 us, 6.8 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 88 us,
 // 6.0 TB/s, its DRAM reads 1.00 of these bytes; a tree of 64 tokens with 8 query
 // heads a key head at 131000 positions 117 us, 1.17 PFLOP/s; one token at 1000
 // positions 10 us, nearly all of it latency: lengths, table, tile, S, P, O and
@@ -44,7 +44,7 @@
 //     shares it is two bf16 numbers (the weight and what rounding left of it),
 //     since with few rows one rounded large weight shows: the result's error is
 //     then that of its own rounding alone.  Without shares it is one, which puts
-//     the error of some hundred rows at 1.2 to 1.3 times that (two would be 1.00,
+//     the error of some hundred rows at 1.2 to 1.4 times that (two would be 1.00,
 //     but 31 against 24 us for 16 trees of 16 to 4000, 149 against 112 for a tree
 //     of 64 at 131000).
 //   * O is corrected only when a row's maximum has grown by more than 8 powers
@@ -404,7 +404,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             W = N;
         }
     } else if (warp == 1) {
-        // ---- MMA: one thread issues, in the order of the ring ----
+        // ---- MMA: one warp issues, in the order of the ring ----
         if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
         constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
