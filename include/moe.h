@@ -604,10 +604,12 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  * workspace is ready for the next call.
  * Lengths, offsets, table and mask are read on the device, so a captured
  * call follows their contents.  Results repeat bit for bit.
- * Products and sums are fp32; bf16: the exponentials are rounded to bf16
- * before the product with V, their sum is not (tensor cores: heads of 64 or
- * 128 and pages that are a multiple of 8 and divide 128 or are a multiple of
- * it; other heads and pages, and fp32, run on CUDA cores).
+ * Products and sums are fp32.  Tensor cores (bf16, heads of 64 or 128, pages
+ * that are a multiple of 8 and divide 128 or are a multiple of it): the
+ * exponentials are rounded before the product with V, their sum is not; to two
+ * bf16 numbers each (2^-16) while the requests have few rows a key head (up to
+ * 48 on average; tokens times heads / kv_heads), to one (2^-9) with more.
+ * Other heads and pages, and fp32, run on CUDA cores, without that rounding.
  * n_requests at most MOE_MAX_REQUESTS, max_pages * page_size at most 2^30.
  */
 typedef struct {
