@@ -27,6 +27,8 @@ __device__ __forceinline__ float ex2(float x) {
 // 27.1 us for 16 trees of 16 to 4000).
 __host__ __device__ constexpr int steps_before(int cost) { return cost - cost * 2 / 5; }
 
+constexpr int kMostSteps = 0x7fffff00;   // of a line: places and their sums with a few more stay below 2^31
+
 // The line of `total` steps in `ranges` equal stretches (the first ones a
 // step longer where it does not divide).
 struct Line {
@@ -57,7 +59,7 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, b
     bad = q.t0 < 0 || t1 > a.T || t1 < q.t0 ||
           (q.n > 0 && (q.ctx < 0 || (long long)q.ctx + q.n > (long long)a.max_pages * a.page_size));
     if (bad) q.n = 0;
-    q.nrt = (q.n * a.group + kRows - 1) / kRows;
+    q.nrt = (int)(((uint32_t)(q.n * a.group) + kRows - 1) / kRows);
     q.nkt = q.n > 0 ? (q.ctx + q.n + kKeys - 1) / kKeys : 0;
     return q;
 }
@@ -65,7 +67,7 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, b
 // Where a CTA's range starts (request, unit, steps into the unit) and how long
 // it is; in shared memory, written by find_start.
 struct LineStart {
-    int scan[16];
+    long long scan[16];
     int r, t0, n, ctx, nrt, nkt, h, rt, off, left;
 };
 
@@ -151,25 +153,39 @@ __device__ __forceinline__ void find_start(const AttentionArgs& a, LineStart& S)
         if (bad && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
         work += (long long)q.nrt * (q.nkt + kUnitCost) * a.kv_heads;
     }
-    // the line's length fits 31 bits (more key tiles than the card's memory holds do not)
-    const bool over = __syncthreads_or(work > 0x7fffffff / kThreads);
-    if (over && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
-    const int sum = over ? 0 : (int)work;
-    int inc = sum;
+    // Places on the line take 31 bits.  The sums are taken in 64 where a
+    // thread's part does not show that they fit (row tiles multiply key tiles,
+    // so one long request can have most of the line); a line that is longer
+    // (the limit stated at moe_tree_attention) gives no work.
+    int before, total, sum = (int)work;
+    auto scan = [&](auto zero) {
+        using N = decltype(zero);
+        N* warps = reinterpret_cast<N*>(S.scan);
+        N inc = (N)work;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, inc, off);
-        if ((int)(threadIdx.x & 31) >= off) inc += t;
-    }
-    if ((threadIdx.x & 31) == 31) S.scan[threadIdx.x >> 5] = inc;
-    __syncthreads();
-    int before = inc - sum, total = 0;
+        for (int off = 1; off < 32; off <<= 1) {
+            const N t = __shfl_up_sync(0xffffffffu, inc, off);
+            if ((int)(threadIdx.x & 31) >= off) inc += t;
+        }
+        if ((threadIdx.x & 31) == 31) warps[threadIdx.x >> 5] = inc;
+        __syncthreads();
+        N b = inc - (N)work, n = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const int t = S.scan[w];
-        if (w < (int)(threadIdx.x >> 5)) before += t;
-        total += t;
-    }
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const N t = warps[w];
+            if (w < (int)(threadIdx.x >> 5)) b += t;
+            n += t;
+        }
+        if (sizeof(N) > 4 && n > kMostSteps) {
+            if (threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
+            b = n = 0;
+            sum = 0;
+        }
+        before = (int)b;
+        total = (int)n;
+    };
+    if (__builtin_expect(!__syncthreads_or(work > kMostSteps / kThreads), 1)) scan(0);
+    else scan(0LL);
     // (no range of a few steps where that makes many parts of many rows)
     const int ranges = min((int)gridDim.x, (total + a.min_steps - 1) / a.min_steps);
     const Line line(total, ranges);
