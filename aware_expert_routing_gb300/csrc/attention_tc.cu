@@ -75,6 +75,9 @@ constexpr uint32_t kOCol = 256;   // tensor memory: S buffers at 0 and 128, O fr
 // to 8000 87.7 / 88.3 / 89.0, 38 trees of 12 to 7666 54.1 / 54.7 / 56.4, one token
 // at 1000 9.6 / 9.6 / 9.4; 6 and 8 were no better.
 constexpr int kUnitCost = 4;
+// Polls of the last waits, for copies and products that run already: these end
+// within microseconds, and the limit is there for a device that has failed.
+constexpr uint32_t kDrainPolls = 1u << 20;
 constexpr float kLazy = 8.f;   // powers of two that P may grow before O is corrected
 
 // Whole warp: lane l receives consecutive 32-bit columns of TMEM lane
@@ -235,10 +238,11 @@ struct Cfg {
 };
 
 struct Control {
-    uint64_t full[16], empty[16], q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2];
+    uint64_t full[16], empty[16], q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2], drained;
     long long wait_cycles;
     LineStart start;
     int abort_flag;
+    uint32_t armed;            // stages filled, or being filled, so far
     uint32_t tmem_base;
     float2 ml[kRowsTile];      // shares' maxima and sums, when they meet
     uint32_t bad[2][2][4];     // per row tile and key tile's parity: keys whose value is not finite
@@ -314,8 +318,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             mbar_init(&S.p_full[i], 4);
             mbar_init(&S.pv_done[i], 1);
         }
+        mbar_init(&S.drained, 1);
         fence_barrier_init();
         S.abort_flag = 0;
+        S.armed = 0;
         S.wait_cycles = a.wait_cycles;
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
@@ -371,7 +377,10 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             ++seq;
             const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
             if (warp_aborted(S)) return;
-            if (lane == 0) mbar_arrive_expect_tx(&S.full[st], n * bytes);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&S.full[st], n * bytes);
+                S.armed = seq;
+            }
             __syncwarp();
             if (g >= 0) tma_load_4d(smem_u32(ring + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &S.full[st]);
         };
@@ -457,6 +466,7 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
         };
         // Once a wait has given up, all return at once: the loop then runs out on
         // whatever the shared and tensor memory hold, which harms nothing.
+        // (Leaving it early costs a vote a tile: 3 % for a tree of 64 tokens.)
         do {
             const int nw = uniform(kTiles == 2 && rows_of(W, 1) > 0 ? 2 : 1);
             const int n = uniform(W.nk);
@@ -928,12 +938,21 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
             }
         }
     }
-    if (aborted(S)) {   // copies that no MMA waited for land before the shared memory is released
-        const long long t0 = clock64();
-        while (clock64() - t0 < 40000) __nanosleep(1000);
-    }
     tmem_fence_before_sync();
     __syncthreads();
+    if (aborted(S)) {   // (nobody sets it any more)
+        // Copies and products that nobody waited for end before the shared and
+        // the tensor memory are released: the last copy into each stage, and a
+        // commit behind all MMAs.
+        if (warp == 0)
+            for (uint32_t i = S.armed > C::kStages ? S.armed - C::kStages : 0; i < S.armed; ++i)
+                mbar_wait(&S.full[i % C::kStages], (i / C::kStages) & 1, kDrainPolls);
+        if (warp == 1) {
+            mma_commit(smem_u32(&S.drained));
+            mbar_wait(&S.drained, 0, kDrainPolls);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tmem_fence_after_sync();
         tmem_dealloc(tmem, 512);
