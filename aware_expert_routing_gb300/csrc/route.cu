@@ -353,7 +353,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& a, const SelectArgs&
             store_token(a, sm, i, il, lane, n, id, w);
             continue;
         }
-        load_keys<NPL>(logits + (size_t)i * N, N, lane, kv, nonfinite);
+        if (kPick == kPlain) load_keys<NPL>(logits + (size_t)i * N, N, lane, kv, nonfinite);
         if (kPick != kPlain || i >= a.B_valid) {   // padding token: selects nothing
             if (lane == 0) {
                 sm.snb[il] = 0;

@@ -417,7 +417,8 @@ moe_status moe_decode_layer(const void *hidden, const void *w_router, const floa
  * A softmax without a bias and with group_top 1 is ranked by x itself,
  * which it keeps in order.  An expert whose x or v is not finite is never
  * chosen (a token may then keep fewer than k experts) and raises
- * MOE_FLAG_NONFINITE_SCORE.  All arithmetic is fp32.
+ * MOE_FLAG_NONFINITE_SCORE; what the scores of padding tokens (B_valid and on)
+ * hold does not matter.  All arithmetic is fp32.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
