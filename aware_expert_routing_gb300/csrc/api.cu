@@ -571,10 +571,10 @@ moe_status resolve_select(const moe_select_params* in, const float* bias, const 
     if (!aligned(bias, 4)) return fail(MOE_ERR_ARG, "select_bias not 4-byte aligned");
     S.bias = bias;
     S.sigmoid = in->score == MOE_SCORE_SIGMOID;
-    // all groups stay: as without groups
+    // all groups stay: as without groups (group_top still says what ranks a softmax)
     S.n_group = in->topk_group == in->n_group ? 1 : in->n_group;
     S.topk_group = in->topk_group;
-    S.group_top = S.n_group == 1 ? 1 : in->group_top;
+    S.group_top = in->group_top;
     S.renorm = in->renormalise;
     S.scale = in->scale;
     return MOE_OK;

@@ -1,4 +1,5 @@
-"""Edges of the grouped selection: padding tokens whose scores hold anything."""
+"""Edges of the grouped selection: padding tokens whose scores hold anything,
+and which values rank a softmax when every group stays."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +48,21 @@ def test_hidden_states_of_padding_tokens_are_not_looked_at(B):
     assert moe.moe_device_status(ws) == 0
     assert (r.expert_idx[valid:] == -1).all() and (r.expert_idx[:valid] >= 0).all()
     assert (r.n_base.cpu() == torch.tensor([4] * valid + [0] * 3)).all()
+
+
+@pytest.mark.parametrize("B", [2, 30])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_a_softmax_with_sums_of_two_is_ranked_by_its_values(B, groups):
+    """group_top 2: experts whose softmax underflows to the same value go by the lower id, also where every group
+    stays; with group_top 1 the scores themselves rank them."""
+    N, k = 8, 3
+    x = torch.full((B, N), -400.0)
+    x[:, 0], x[:, 5], x[:, 7] = 0.0, -150.0, -200.0
+    prm = moe.RouteParams(B=B, d=256, N=N, k=k)
+    ws = moe.alloc_workspace(prm, 0, DEV)
+    for top, want in ((2, [0, 1, 2]), (1, [0, 5, 7])):
+        r = moe.Routing(prm, DEV)
+        moe.moe_route_scores(x.to(DEV), None, prm, moe.SelectParams(n_group=groups, topk_group=groups, group_top=top), r, ws)
+        assert moe.moe_device_status(ws) == 0
+        assert r.expert_idx.cpu().tolist() == [want] * B, top
+        assert r.weights.cpu().tolist() == [[1.0, 0.0, 0.0]] * B
