@@ -193,7 +193,9 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         moe_attention_params p{};
         const at::Tensor* mask = dense(a[3], at::kInt, "mask", true);
         if (mask) {
-            if (mask->dim() != 2 || mask->size(0) != T) refuse("mask must be [%lld][words]", (long long)T);
+            // (an empty tensor's pointer is null, which the C ABI takes for no mask)
+            if (mask->dim() != 2 || mask->size(0) != T || (T > 0 && mask->size(1) < 1))
+                refuse("mask must be [%lld][words], of one word at least", (long long)T);
             p.mask_words = narrow(mask->size(1), "mask_words");
         }
         const at::Tensor* ws = dense(a[7], at::kByte, "workspace");
