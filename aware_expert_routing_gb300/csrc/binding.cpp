@@ -67,6 +67,9 @@ const at::Tensor& rows(PyObject* o, at::ScalarType type, int64_t T, int64_t head
     return t;
 }
 
+// The distance along a dimension; one of size 1 has none (its stride may be any number).
+int64_t distance(const at::Tensor& t, int64_t dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
 const void* ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 // None: the tensor's device's current stream; else a torch.cuda.Stream.
@@ -143,10 +146,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q = &rows(a[0], dt, T, heads, D, "q");
             out = &rows(a[7], dt, T, heads, D, "q_out");
             p.heads = narrow(heads, "heads");
-            p.q_tok = q->stride(0);
-            p.q_head = q->stride(1);
-            p.out_tok = out->stride(0);
-            p.out_head = out->stride(1);
+            p.q_tok = distance(*q, 0);
+            p.q_head = distance(*q, 1);
+            p.out_tok = distance(*out, 0);
+            p.out_head = distance(*out, 1);
         }
         const at::Tensor *rope = dense(a[3], at::kFloat, "rope", true), *pos = nullptr;
         if (rope) {
@@ -163,10 +166,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int inter = PyObject_IsTrue(a[9]);
         if (inter < 0) throw Bad{};
         p.interleaved = inter;
-        p.k_tok = k.stride(0);
-        p.k_head = k.stride(1);
-        p.v_tok = v.stride(0);
-        p.v_head = v.stride(1);
+        p.k_tok = distance(k, 0);
+        p.k_head = distance(k, 1);
+        p.v_tok = distance(v, 0);
+        p.v_head = distance(v, 1);
         return moe_kv_append(ptr(q), k.data_ptr(), v.data_ptr(), static_cast<const float*>(ptr(rope)),
                              static_cast<const int32_t*>(ptr(pos)), static_cast<const int64_t*>(ptr(slots)), &p, c,
                              const_cast<void*>(ptr(out)), ws->data_ptr(), (size_t)ws->numel(), stream_of(a[10], k));
@@ -207,8 +210,8 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             p.scale = (float)PyFloat_AsDouble(a[8]);
             if (PyErr_Occurred()) throw Bad{};
         }
-        p.q_tok = q.stride(0);
-        p.q_head = q.stride(1);
+        p.q_tok = distance(q, 0);
+        p.q_head = distance(q, 1);
         return moe_tree_attention(q.data_ptr(), static_cast<const int32_t*>(ptr(off)), static_cast<const int32_t*>(ptr(ctx)),
                                   static_cast<const uint32_t*>(ptr(mask)), &p, c, out->data_ptr(),
                                   static_cast<float*>(const_cast<void*>(ptr(lse))), ws->data_ptr(), (size_t)ws->numel(),

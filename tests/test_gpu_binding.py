@@ -31,3 +31,40 @@ def test_a_mask_without_words_is_refused():
     # a call without tokens has a mask without words (tree_mask([]))
     none = q[:0].contiguous()
     moe.moe_tree_attention(none, torch.zeros_like(off), ctx, moe.tree_mask([]).to(DEV), c, torch.empty_like(none), None, ws)
+
+
+def odd(shape, stride, values):
+    """The values in a tensor with the given distances."""
+    t = torch.zeros(4096, dtype=values.dtype, device=DEV).as_strided(shape, stride)
+    t.copy_(values)
+    return t
+
+
+@pytest.mark.parametrize("T,H", [(1, 4), (1, 2), (3, 2)])
+def test_the_distance_of_a_single_token_or_head_does_not_matter(T, H):
+    """A dimension of size 1 may have any distance (slices of a wider row, expanded tensors)."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = (torch.randn(T, h, 64, generator=g, device=DEV).to(torch.bfloat16) for h in (H, 2, 2))
+    tok, head = (333 if T == 1 else 320), 64
+    out = []
+    for qq, kk, vv in ((q, k, v), (odd((T, H, 64), (tok, head, 1), q), odd((T, 2, 64), (tok, head, 1), k),
+                                   odd((T, 2, 64), (tok, head, 1), v))):
+        c = cache()
+        ws = moe.alloc_attention_workspace(T, H, c, DEV)
+        rope = moe.moe_rope_table(moe.RopeParams(rot=64), 32, DEV)
+        pos = torch.arange(T, dtype=torch.int32, device=DEV)
+        rot = torch.empty(T, H, 64, dtype=torch.bfloat16, device=DEV)
+        moe.moe_kv_append(qq, kk, vv, rope, pos, 5 + pos.long(), c, rot, ws)
+        o = torch.empty_like(rot)
+        off, ctx = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, T, T], [5, 0]))
+        moe.moe_tree_attention(qq, off, ctx, None, c, o, None, ws)
+        assert moe.moe_device_status(ws) == 0
+        out.append((rot, c.k, c.v, o))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    # one key head, its distance odd
+    one = torch.randn(T, 1, 64, generator=g, device=DEV).to(torch.bfloat16)
+    ck = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(512, dtype=torch.uint8, device=DEV)
+    w = odd((T, 1, 64), (320, 77, 1), one)
+    moe.moe_kv_append(None, w, w, None, None, torch.arange(T, device=DEV), moe.KvCache(ck, ck.clone()), None, ws)
+    assert moe.moe_device_status(ws) == 0 and torch.equal(ck[0, 0, :T], one[:, 0])
