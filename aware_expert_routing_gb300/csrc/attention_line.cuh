@@ -27,8 +27,6 @@ __device__ __forceinline__ float ex2(float x) {
 // 27.1 us for 16 trees of 16 to 4000).
 __host__ __device__ constexpr int steps_before(int cost) { return cost - cost * 2 / 5; }
 
-constexpr int kMostSteps = 0x7fffff00;   // of a line: places and their sums with a few more stay below 2^31
-
 // The line of `total` steps in `ranges` equal stretches (the first ones a
 // step longer where it does not divide).
 struct Line {
@@ -67,7 +65,7 @@ __device__ __forceinline__ Request load_request(const AttentionArgs& a, int r, b
 // Where a CTA's range starts (request, unit, steps into the unit) and how long
 // it is; in shared memory, written by find_start.
 struct LineStart {
-    long long scan[16];
+    uint2 scan[16];
     int r, t0, n, ctx, nrt, nkt, h, rt, off, left;
 };
 
@@ -153,39 +151,31 @@ __device__ __forceinline__ void find_start(const AttentionArgs& a, LineStart& S)
         if (bad && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
         work += (long long)q.nrt * (q.nkt + kUnitCost) * a.kv_heads;
     }
-    // Places on the line take 31 bits.  The sums are taken in 64 where a
-    // thread's part does not show that they fit (row tiles multiply key tiles,
-    // so one long request can have most of the line); a line that is longer
-    // (the limit stated at moe_tree_attention) gives no work.
-    int before, total, sum = (int)work;
-    auto scan = [&](auto zero) {
-        using N = decltype(zero);
-        N* warps = reinterpret_cast<N*>(S.scan);
-        N inc = (N)work;
+    // Places on the line take 31 bits, and so do their sums, modulo 2^32, if the
+    // total does: row tiles multiply key tiles, so one long request can have most
+    // of the line.  Whether it does is told by a second sum, of 2^16 steps each
+    // (rounded down, kThreads times): a longer line (the limit stated at
+    // moe_tree_attention) gives no work.
+    uint32_t inc = (uint32_t)work;
+    const uint32_t thick = __reduce_add_sync(0xffffffffu, (uint32_t)min(work >> 16, 1LL << 20));
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const N t = __shfl_up_sync(0xffffffffu, inc, off);
-            if ((int)(threadIdx.x & 31) >= off) inc += t;
-        }
-        if ((threadIdx.x & 31) == 31) warps[threadIdx.x >> 5] = inc;
-        __syncthreads();
-        N b = inc - (N)work, n = 0;
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, inc, off);
+        if ((int)(threadIdx.x & 31) >= off) inc += t;
+    }
+    if ((threadIdx.x & 31) == 31) S.scan[threadIdx.x >> 5] = make_uint2(inc, thick);
+    __syncthreads();
+    uint32_t first = inc - (uint32_t)work, all = 0, all_thick = kThreads;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const N t = warps[w];
-            if (w < (int)(threadIdx.x >> 5)) b += t;
-            n += t;
-        }
-        if (sizeof(N) > 4 && n > kMostSteps) {
-            if (threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
-            b = n = 0;
-            sum = 0;
-        }
-        before = (int)b;
-        total = (int)n;
-    };
-    if (__builtin_expect(!__syncthreads_or(work > kMostSteps / kThreads), 1)) scan(0);
-    else scan(0LL);
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const uint2 t = S.scan[w];
+        if (w < (int)(threadIdx.x >> 5)) first += t.x;
+        all += t.x;
+        all_thick += t.y;
+    }
+    const bool over = all_thick > 0x7fff;
+    if (over && threadIdx.x == 0 && blockIdx.x == 0) raise_flag(a.flags, kFlagBadIndex);
+    const int before = (int)first, total = over ? 0 : (int)all, sum = (int)(uint32_t)work;
     // (no range of a few steps where that makes many parts of many rows)
     const int ranges = min((int)gridDim.x, (total + a.min_steps - 1) / a.min_steps);
     const Line line(total, ranges);

@@ -612,11 +612,11 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  * 48 on average; tokens times heads / kv_heads), to one (2^-9) with more.
  * Other heads and pages, and fp32, run on CUDA cores, without that rounding.
  * n_requests at most MOE_MAX_REQUESTS, max_pages * page_size at most 2^30.
- * One call takes up to 2^31 - 256 pairs of a tile of query rows (tokens times
+ * One call takes up to 2^31 - 2^25 pairs of a tile of query rows (tokens times
  * heads / kv_heads, of one request and key head; the shorter the requests, the
  * smaller the tiles) and a tile of keys: minutes of work, such as a prompt of
  * 2^20 tokens with 64 heads, tiles of 256 rows and 128 keys, or on CUDA cores one
- * of 2^18 (64 rows, 32 keys).  Past that MOE_FLAG_BAD_INDEX is raised and no
+ * of 2^18 (64 rows, 32 keys).  From 2^31 on MOE_FLAG_BAD_INDEX is raised and no
  * output of the call is written.
  */
 typedef struct {
