@@ -12,7 +12,7 @@
 #include <string>
 #include <unordered_map>
 
-#include "common.cuh"
+#include "route.cuh"
 
 using namespace moe;
 
@@ -656,8 +656,8 @@ moe_status route_impl(const void* hidden, const void* w_router, const float* rou
         a.uwords = hdr->union_words;
         a.epoch = next_epoch();
     }
-    const SelectArgs* sel = select ? &sa : nullptr;
-    e = fused ? launch_route_fused(ra, a, sel, s) : launch_route(a, sel, s);
+    e = select ? fused ? launch_route_fused(ra, a, sa, s) : launch_route(a, sa, s)
+               : fused ? launch_route_fused(ra, a, s) : launch_route(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "route launch");
     routed(workspace, a.epoch);   // an expert call on this workspace now waits for it
     return MOE_OK;

@@ -113,15 +113,6 @@ struct RouteArgs {
     uint32_t* clr_hdone;
 };
 
-// Selection of moe_select_params (top-k mode only).
-struct SelectArgs {
-    const float* bias;      // [N] or null, added to the selection values
-    int sigmoid;            // 1: sigmoid scores, 0: softmax
-    int n_group, topk_group, group_top;
-    int renorm;
-    float scale;
-};
-
 struct FfnArgs {
     const void* x;          // [B][d] hidden
     const int32_t* T;
@@ -173,12 +164,11 @@ long long wait_cycles_now();
 
 // Launchers (defined in the .cu files).
 cudaError_t launch_router(const RouterArgs& a, int dtype, cudaStream_t s);
-// sel null: plain top-k or OEA.
-cudaError_t launch_route(const RouteArgs& a, const SelectArgs* sel, cudaStream_t s);
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 // Router scores and routing in one cluster launch (bf16, up to 32 tokens,
 // N <= 128); launch_router + launch_route otherwise.
 bool route_fused_supported(int dtype, int B, int N, int kslots);
-cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, const SelectArgs* sel, cudaStream_t s);
+cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, cudaStream_t s);
 // tcgen05 expert kernel (bf16 weights).  maps[0..6]: W_gate/W_up
 // interleaved 8 rows at a time (5D, gu_fused) or W_gate alone (8-row
 // boxes), the same again (not read), W_up (8-row boxes), W_down (128-row

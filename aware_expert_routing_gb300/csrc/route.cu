@@ -42,7 +42,7 @@
 // router kernel.
 #include <limits.h>
 
-#include "common.cuh"
+#include "route.cuh"
 
 namespace moe {
 
@@ -880,15 +880,20 @@ constexpr int kOwnSelection = 12;
 
 }  // namespace
 
-cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
-    return sel ? launch_route_fused_s<kSelect>(r, a, *sel, s) : launch_route_fused_s<kPlain>(r, a, SelectArgs{}, s);
+cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, cudaStream_t s) {
+    return launch_route_fused_s<kPlain>(r, a, SelectArgs{}, s);
 }
 
-cudaError_t launch_route(const RouteArgs& a, const SelectArgs* sel, cudaStream_t s) {
-    if (!sel) return launch_route_s<kPlain>(a, SelectArgs{}, s);
-    if (a.B < kOwnSelection) return launch_route_s<kSelect>(a, *sel, s);
-    const cudaError_t e = launch_select(a, *sel, s);
-    return e == cudaSuccess ? launch_route_s<kGiven>(a, *sel, s) : e;
+cudaError_t launch_route_fused(const RouterArgs& r, const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
+    return launch_route_fused_s<kSelect>(r, a, sel, s);
+}
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) { return launch_route_s<kPlain>(a, SelectArgs{}, s); }
+
+cudaError_t launch_route(const RouteArgs& a, const SelectArgs& sel, cudaStream_t s) {
+    if (a.B < kOwnSelection) return launch_route_s<kSelect>(a, sel, s);
+    const cudaError_t e = launch_select(a, sel, s);
+    return e == cudaSuccess ? launch_route_s<kGiven>(a, sel, s) : e;
 }
 
 }  // namespace moe
