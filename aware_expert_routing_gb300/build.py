@@ -2,8 +2,10 @@
 
 Each .cu file is compiled in parallel, then linked into one shared library
 next to this file; binding.cpp becomes the extension module _binding.so,
-which links to it.  Set MOE_PTXAS_VERBOSE=1 to print register and shared
-memory usage per kernel.
+which links to it.  The library needs nvcc only: without g++ on the path, torch
+or Python's headers the module is left out, which callers of the C ABI do
+without.  Set MOE_PTXAS_VERBOSE=1 to print register and shared memory usage per
+kernel.
 """
 from __future__ import annotations
 
@@ -33,9 +35,19 @@ def nvcc() -> str:
     return path
 
 
+def binding_lacks() -> str:
+    """What building the extension module wants and this machine has not."""
+    if not shutil.which("g++"):
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return "" if importlib.util.find_spec("torch") else "torch"
+
+
 def compile_binding(obj: str):
     """binding.cpp with the host compiler, against Python's, torch's and
-    CUDA's headers."""
+    CUDA's headers.  Returns the folder of torch's libraries; raises if the
+    code does not compile."""
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -54,9 +66,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] if binding_lacks() else [LIB, BINDING]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
 
 
@@ -80,16 +93,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     bind = os.path.join(BUILD, "binding.o")
+    lacks = binding_lacks()
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_lib = ex.submit(compile_binding, bind)
+        binding = None if lacks else ex.submit(compile_binding, bind)
         objs = list(ex.map(compile_one, SOURCES))
-        torch_lib = torch_lib.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname," + os.path.basename(LIB), "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the library stands, whatever becomes of the module
+    if lacks:
+        sys.stderr.write(f"{os.path.basename(BINDING)} left out (the per-token Python calls need it): no {lacks}\n")
+        return LIB
+    torch_lib = binding.result()
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, bind, "-L" + HERE, "-l:" + os.path.basename(LIB), "-L" + torch_lib,
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
