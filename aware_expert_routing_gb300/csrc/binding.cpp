@@ -255,23 +255,29 @@ PyObject* route_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* bias = dense(a[1], at::kFloat, "select_bias", true);
         if (bias && bias->numel() != p.N) refuse("select_bias must hold %d values", p.N);
         const at::Tensor* ws = dense(a[5], at::kByte, "workspace");
-        // the routing's buffers are its own; it holds them while this call runs
-        auto buffer = [&](Name name) -> void* {
+        // The routing's buffers are its own; it holds them while this call runs.
+        // One made for a smaller batch or fewer experts is refused.
+        auto buffer = [&](Name name, at::ScalarType type, int64_t least) -> void* {
             PyObject* o = PyObject_GetAttr(a[4], g_names[name]);
             if (!o) throw Bad{};
-            void* q = o == Py_None ? nullptr : THPVariable_Check(o) ? THPVariable_Unpack(o).data_ptr() : nullptr;
-            Py_DECREF(o);
-            return q;
+            struct Held {
+                PyObject* o;
+                ~Held() { Py_DECREF(o); }
+            } held{o};
+            const at::Tensor* t = dense(o, type, kText[name], name == kNBase);
+            if (t && t->numel() < least) refuse("the routing's %s must hold %lld values", kText[name], (long long)least);
+            return t ? t->data_ptr() : nullptr;
         };
+        const int64_t pairs = (int64_t)p.B * p.k, N = p.N;   // (top-k mode: k slots a token)
         moe_routing r{};
-        r.expert_idx = static_cast<int32_t*>(buffer(kExpertIdx));
-        r.weights = static_cast<float*>(buffer(kWeights));
-        r.T = static_cast<int32_t*>(buffer(kT));
-        r.active = static_cast<int32_t*>(buffer(kActive));
-        r.counts = static_cast<int32_t*>(buffer(kCounts));
-        r.offsets = static_cast<int32_t*>(buffer(kOffsets));
-        r.perm = static_cast<int32_t*>(buffer(kPerm));
-        r.n_base = static_cast<int32_t*>(buffer(kNBase));
+        r.expert_idx = static_cast<int32_t*>(buffer(kExpertIdx, at::kInt, pairs));
+        r.weights = static_cast<float*>(buffer(kWeights, at::kFloat, pairs));
+        r.T = static_cast<int32_t*>(buffer(kT, at::kInt, 1));
+        r.active = static_cast<int32_t*>(buffer(kActive, at::kInt, N));
+        r.counts = static_cast<int32_t*>(buffer(kCounts, at::kInt, N));
+        r.offsets = static_cast<int32_t*>(buffer(kOffsets, at::kInt, N + 1));
+        r.perm = static_cast<int32_t*>(buffer(kPerm, at::kInt, pairs));
+        r.n_base = static_cast<int32_t*>(buffer(kNBase, at::kInt, p.B));
         return moe_route_scores(static_cast<const float*>(ptr(x)), static_cast<const float*>(ptr(bias)), &p, &s, &r,
                                 ws->data_ptr(), (size_t)ws->numel(), stream_of(a[6], *x));
     });

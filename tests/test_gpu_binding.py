@@ -68,3 +68,29 @@ def test_the_distance_of_a_single_token_or_head_does_not_matter(T, H):
     w = odd((T, 1, 64), (320, 77, 1), one)
     moe.moe_kv_append(None, w, w, None, None, torch.arange(T, device=DEV), moe.KvCache(ck, ck.clone()), None, ws)
     assert moe.moe_device_status(ws) == 0 and torch.equal(ck[0, 0, :T], one[:, 0])
+
+
+@pytest.mark.parametrize("kw", [dict(B=4), dict(N=32), dict(k=2)])
+def test_a_routing_of_another_size_is_refused(kw):
+    prm = moe.RouteParams(**{**dict(B=8, d=256, N=64, k=4), **kw})
+    small = moe.Routing(prm, DEV)
+    prm = moe.RouteParams(B=8, d=256, N=64, k=4)
+    ws = moe.alloc_workspace(prm, 0, DEV)
+    x = torch.randn(8, 64, device=DEV)
+    with pytest.raises(ValueError):
+        moe.moe_route_scores(x, None, prm, moe.SelectParams(), small, ws)
+    good = moe.Routing(prm, DEV)
+    moe.moe_route_scores(x, None, prm, moe.SelectParams(), good, ws)      # and one of this size serves, or a larger one
+    want = good.expert_idx.clone()
+    large = moe.Routing(moe.RouteParams(B=16, d=256, N=64, k=4), DEV)
+    moe.moe_route_scores(x, None, prm, moe.SelectParams(), large, ws)
+    assert torch.equal(large.expert_idx[:8], want)
+    for name in ("counts", "weights"):
+        bad = moe.Routing(prm, DEV)
+        setattr(bad, name, getattr(bad, name).double())
+        with pytest.raises(ValueError):
+            moe.moe_route_scores(x, None, prm, moe.SelectParams(), bad, ws)
+    bad = moe.Routing(prm, DEV)
+    bad.perm = None
+    with pytest.raises(ValueError):
+        moe.moe_route_scores(x, None, prm, moe.SelectParams(), bad, ws)
