@@ -694,7 +694,8 @@ def moe_tree_attention(q, q_offsets, ctx_len, mask, cache: KvCache, out, lse, wo
     caches: request r's tokens q_offsets[r]..q_offsets[r+1]-1 see its first
     ctx_len[r] positions, and of the step's own tokens those that mask ([T]
     [words] int32 bits) allows (None: the token itself and those before it).
-    scale: 1 / sqrt(head_dim) by default.  lse may be None."""
+    scale: 1 / sqrt(head_dim) by default.  lse may be None.  A cache whose page
+    table has about as many rows as requests that take part serves best."""
     st = (_fast or _load_binding()).tree_attention(q, q_offsets, ctx_len, mask, cache._at, out, lse, workspace, scale, stream)
     if st:
         _check(st, "moe_tree_attention")

@@ -8,10 +8,12 @@
 //
 // Here: the entry point, and the kernel on CUDA cores that serves what the
 // tensor cores (attention_tc.cu) do not: fp32, and bf16 heads or pages of
-// other sizes.  fp32 has no tensor-core path that keeps fp32's accuracy, so its
-// bound is the FMA rate (74 TFLOP/s at 1.9 GHz) from about 11 query rows a key
-// head on, and the cache's bytes below.  Measured, 4 trees of 7 tokens up to
-// 2000 positions, 8 + 2 heads of 64: 14.6 us, of which the bytes would take 0.6;
+// other sizes.  Its bound is the FMA rate (74 TFLOP/s at 1.9 GHz) from about 11
+// query rows a key head on, and the cache's bytes below.  (fp32 on tensor cores
+// would take its operands in three bf16 parts and six products; not built, and
+// neither are tiles for the other bf16 heads and pages.)  Measured, 4 chains of 7
+// tokens up to 2000 positions, 8 + 2 heads of 64: 14.8 us, of which the bytes
+// would take 0.6;
 // at this length the steps of one unit (lengths, table, tile, scores, softmax,
 // values) wait for one another.
 #include <type_traits>

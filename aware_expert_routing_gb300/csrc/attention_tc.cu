@@ -10,11 +10,12 @@
 // and at the end O / l.  Keys and values are read once per unit of work, so
 // the cache's bytes bound the kernel while a key head has fewer than about
 // 250 rows, and the chain from S over the softmax to P V above.  Measured, with
-// heads of 128 and 4 key heads: 256 single tokens up to 16000 positions (4.53
-// GB) 665 us, 6.8 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 88 us,
+// heads of 128 and 4 key heads, called back to back (from one card to another up
+// to 4 % apart): 256 single tokens up to 16000 positions (4.53 GB) 648 to 672 us,
+// 6.7 to 7.0 TB/s, as fast as a plain copy; 64 up to 8000 (532 MB) 88 to 89 us,
 // 6.0 TB/s, its DRAM reads 1.00 of these bytes; a tree of 64 tokens with 8 query
-// heads a key head at 131000 positions 117 us, 1.17 PFLOP/s; one token at 1000
-// positions 10 us, nearly all of it latency: lengths, table, tile, S, P, O and
+// heads a key head at 131000 positions 117 to 120 us, 1.17 PFLOP/s; one token at
+// 1000 positions 10 us, nearly all of it latency: lengths, table, tile, S, P, O and
 // the join one after the other.
 //
 //   * Work.  A unit is (request, key head, tile of rows); its key tiles follow
@@ -43,10 +44,10 @@
 //   * P replaces S in tensor memory and is the A operand of P V, in bf16.  With
 //     shares it is two bf16 numbers (the weight and what rounding left of it),
 //     since with few rows one rounded large weight shows: the result's error is
-//     then that of its own rounding alone.  Without shares it is one, which puts
-//     the error of some hundred rows at 1.2 to 1.4 times that (two would be 1.00,
-//     but 31 against 24 us for 16 trees of 16 to 4000, 149 against 112 for a tree
-//     of 64 at 131000).
+//     then that of its own rounding alone.  Without shares it is one (off by up to
+//     2^-8 of it), which puts the error of some hundred rows at 1.2 to 1.4 times
+//     that (two would be 1.00, but, replayed from a graph, 31 against 24 us for 16
+//     trees of 16 to 4000, 149 against 112 for a tree of 64 at 131000).
 //   * O is corrected only when a row's maximum has grown by more than 8 powers
 //     of two since the last correction (P then stays below 2^8, exact in the
 //     sums), so almost never after the first tiles.
@@ -1021,10 +1022,14 @@ cudaError_t launch_attention_tc(const AttentionArgs& a, int sms, cudaStream_t s)
     AttentionArgs b = a;
     b.min_steps = two ? 2 : 1;
     // Shares by the requests' rows a key head on average, with room for those
-    // above it, or by the one token that each has.  No shares and P in one bf16 /
-    // in two / shares and two: 64 tokens to 8000 89.2 / 121.0 / 88.4 us, 256 to
-    // 16000 671 / 851 / 642, 15 to 5778 16.0 / 18.5 / 14.7, one at 1000 9.6 / 10.2
-    // / 10.1, 38 trees of 12 with 4 heads a key head 55.2 / 70.3 / 55.8.
+    // above it; T <= R is taken for one token each.  (R counts the page table's
+    // rows without tokens too: where most are, one request's 64 tokens are cut
+    // into units of 16 rows, each of which reads the keys: 94 us against 30 for
+    // three such requests at 4000 positions in a table of 256 rows and of 3.)
+    // In one process, replayed from a graph, no shares and P in one bf16 / in two
+    // / shares and two: 64 tokens to 8000 89.2 / 121.0 / 88.4 us, 256 to 16000 671
+    // / 851 / 642, 15 to 5778 16.0 / 18.5 / 14.7, one at 1000 9.6 / 10.2 / 10.1,
+    // 38 trees of 12 with 4 heads a key head 55.2 / 70.3 / 55.8.
     const long long all = (long long)a.T * a.group;
     const bool even = a.R == 1;   // the mean is all there is
     const int shares = all <= (even ? 16 : 12) * (long long)a.R || (a.T <= a.R && a.group <= 16)   ? 4

@@ -419,6 +419,8 @@ moe_status moe_decode_layer(const void *hidden, const void *w_router, const floa
  * chosen (a token may then keep fewer than k experts) and raises
  * MOE_FLAG_NONFINITE_SCORE; what the scores of padding tokens (B_valid and on)
  * hold does not matter.  All arithmetic is fp32.
+ * MOE_MODE_TOPK only: OEA's two phases are defined on the softmax of the scores
+ * over all experts, and what they should be with groups or a balance bias is not.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
@@ -596,7 +598,8 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  * q_offsets[n_requests] are not written.  What lies in positions that a
  * token does not see, and in rows of its request's pages past its length,
  * has no influence on it whatever its value; a token that sees a drafted
- * token whose value (V) is not finite may become NaN in all components.
+ * token whose value (V) is not finite may become NaN in all components, and one
+ * that sees such a value in the context infinite or NaN in that component.
  * A request whose length does not fit max_pages, whose page is outside
  * 0..n_pages-1, or whose q_offsets or ctx_len are out of range raises
  * MOE_FLAG_BAD_INDEX; its output is unspecified, other requests are not
@@ -608,9 +611,15 @@ moe_status moe_kv_append(const void *q, const void *k, const void *v, const floa
  * Products and sums are fp32.  Tensor cores (bf16, heads of 64 or 128, pages
  * that are a multiple of 8 and divide 128 or are a multiple of it): the
  * exponentials are rounded before the product with V, their sum is not; to two
- * bf16 numbers each (2^-16) while the requests have few rows a key head (up to
- * 48 on average; tokens times heads / kv_heads), to one (2^-9) with more.
- * Other heads and pages, and fp32, run on CUDA cores, without that rounding.
+ * bf16 numbers each (2^-16 of it) while the requests have few rows a key head
+ * (tokens times heads / kv_heads), to one (2^-8 of it) with more.  Few are up to
+ * 48 on average, T over n_requests; up to 64 for one request, or where T is at
+ * most n_requests.  Other heads and pages, and fp32, run on CUDA cores, without
+ * that rounding.
+ * T and n_requests (the page table's height) choose the tiles as well: a table
+ * with many rows for requests that have no tokens in the step, or a T with many
+ * tokens past q_offsets[n_requests], costs time (3 requests of 64 tokens at 4000
+ * positions in a table of 256 rows 94 us, of 3 rows 30), not correctness.
  * n_requests at most MOE_MAX_REQUESTS, max_pages * page_size at most 2^30.
  * One call takes up to 2^31 - 2^25 pairs of a tile of query rows (tokens times
  * heads / kv_heads, of one request and key head; the shorter the requests, the
