@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(kMany ? 64 : 256, kMany ? 24 : 5) append_kerne
     }
 }
 
-// Any even rotation: one thread per pair or component.
+// Any even rotation: one thread per pair or component, in loads of 2 or 4 bytes,
+// which bound it.  bf16, 32 + 2 x 4 heads of 80 components: 16000 tokens 146 us
+// with 20 of them rotated, against 39 in whole words with all (30 at the copy
+// rate); 256 tokens of 64 + 2 x 4 heads 16.8 against 3.4.
 template <typename T>
 __global__ void append_any_kernel(const AppendArgs a) {
     const int t = blockIdx.x;
