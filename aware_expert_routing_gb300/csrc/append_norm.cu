@@ -285,11 +285,13 @@ __device__ __forceinline__ float inverse_root_exact(const NormArgs& n, const uin
     s = two_sum(s, n.deps_hi, err);
     if (!(s < INFINITY)) return __frsqrt_rn(s);   // (squares past fp32: 0, as without; NaN)
     low = __fadd_rn(low, __fadd_rn(err, n.deps_lo));
-    // y = sqrt(D) (1 + u / 2) r, where u = 1 - (s + low) r^2
-    const float r = __frsqrt_rn(s), q = __fmul_rn(r, r), qe = __fmaf_rn(r, r, -q);
-    float u = __fmaf_rn(-s, q, 1.f);
-    u = __fmaf_rn(-s, qe, u);
-    u = __fmaf_rn(-low, q, u);
+    // y = sqrt(D) (1 + u / 2) r, where u = 1 - (s + low) r^2, by way of s r, about the root
+    // of s: r^2 passes fp32 where s is below its smallest normal number (rows of zeros with
+    // a tiny eps), and loses bits where s is near its largest.
+    const float r = __frsqrt_rn(s), q = __fmul_rn(s, r), qe = __fmaf_rn(s, r, -q);
+    float u = __fmaf_rn(-q, r, 1.f);
+    u = __fmaf_rn(-qe, r, u);
+    u = __fmaf_rn(__fmul_rn(-low, r), r, u);
     const float p = __fmul_rn(r, n.root_hi), pe = __fmaf_rn(r, n.root_hi, -p);
     return __fadd_rn(p, __fmaf_rn(0.5f * u, p, __fmaf_rn(r, n.root_lo, pe)));
 }
