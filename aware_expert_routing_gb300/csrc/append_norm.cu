@@ -990,6 +990,7 @@ moe_status moe_kv_append_q8(const void* q, const void* k, const void* v, const f
     const bool bf16 = cache->dtype == MOE_DTYPE_BF16;
     n.a.D = cache->head_dim;
     if ((st = fill_norm(norm, n.a, n)) != MOE_OK || n.a.T == 0) return st;
+    if (norm && !std::isfinite(n.deps_hi)) return report(MOE_ERR_ARG, "eps=%g times head_dim=%d passes fp32", norm->eps, n.a.D);
     n.ks = cache->k_scale;
     n.vs = cache->v_scale;
     n.block = cache->block;

@@ -653,8 +653,8 @@ moe_status moe_tree_attention(const void *q, const int32_t *q_offsets, const int
  *   q_weight, k_weight  [head_dim], or [heads][head_dim] and [kv_heads]
  *             [head_dim] with per_head 1; dtype of q and k, 16-byte aligned;
  *             NULL: ones (offset is not read then).
- *   eps       positive and finite.  offset: 0, or 1 for models that keep the
- *             weights less 1; finite.
+ *   eps       positive and finite (moe_kv_append_q8: eps * head_dim too).
+ *   offset    0, or 1 for models that keep the weights less 1; finite.
  */
 typedef struct {
     const void *q_weight, *k_weight;
