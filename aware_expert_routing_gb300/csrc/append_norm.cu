@@ -499,6 +499,12 @@ __device__ __forceinline__ void block_rows(const NormArgs& n, unsigned char* sme
     const bool in = threadIdx.x < 96 && tw >= 0 && tw < a.T;
     const long long slot_w = in ? a.slots[tw] : -1;
     const int position_w = in && threadIdx.x >= 32 && a.rot > 0 ? a.positions[tw] : 0;
+    if (a.heads == 0 && a.rot > 0 && part == 0 && (int)threadIdx.x < c1 - c0) {   // (with queries these are looked at in plain_rows)
+        // positions of tokens that write nothing; those of others are looked at with their rows
+        const long long slot = a.slots[c0 + threadIdx.x];
+        const int m = a.positions[c0 + threadIdx.x];
+        if ((slot < 0 || slot >= a.n_slots) && (m < 0 || m >= a.n_pos)) raise_flag(a.flags, kFlagBadIndex);
+    }
     if (n.chunk == 1 && n.block > 1 && c0 > 0) {   // most thread blocks find nothing, and make room at once
         const long long mine = block_of(a.slots[c0]);
         if (mine >= 0 && mine == block_of(a.slots[c0 - 1])) return;

@@ -36,3 +36,28 @@ def test_rows_of_zeros_and_large_rows_at_any_eps(dtype, eps):
     assert moe.moe_device_status(ws) == 0
     assert (q_out[3] == 0).all() and (q_out[16:] == 0).all()
     c8.check(c, c.slots, True, c.wk)
+
+
+@pytest.mark.parametrize("T,block", [(9, 8), (9, 1), (300, 8), (300, 1), (1100, 8), (1100, 1)])
+@pytest.mark.parametrize("skip", [-1, 1 << 40])
+@pytest.mark.parametrize("position", [-1, 700])
+def test_positions_of_skipped_tokens_are_checked_without_queries(T, block, skip, position):
+    """The flag does not depend on whether queries are given, nor on the cache's kind."""
+    c = append.Case([(4, T)], 2, 1, 64, 64, 16, layout="own", seed=3)
+    at = T - 4                                  # (a slot past the cache raises the flag by itself: two calls differ)
+    c.slots[at] = skip
+    for bad in (False, True):
+        if bad:
+            c.positions[at] = position
+        q, k, v, rope, pos, slots = c.on_gpu()
+        plain = moe.KvCache(*(torch.zeros(c.P, 1, 16, 64, dtype=c.dt, device=DEV) for _ in range(2)))
+        want = moe.FLAG_BAD_INDEX if bad or skip > 0 else 0
+        q_out = torch.empty_like(q)
+        for qs in ((None, None), (q, q_out)):
+            c8 = append.Cache8(c, block, 2)
+            ws = append.workspace()
+            moe.moe_kv_append_q8(qs[0], k, v, rope, pos, slots, c.norm, c8.gpu, qs[1], ws)
+            assert moe.moe_device_status(ws) == want
+            moe.moe_kv_append_norm(qs[0], k, v, rope, pos, slots, c.norm, plain, qs[1], ws)
+            assert moe.moe_device_status(ws) == want
+            c8.check(c, c.slots, True, c.wk)
