@@ -709,7 +709,7 @@ class KvCacheQ8:
                              page_table.data_ptr() if page_table is not None else None, self.n_pages, self.page_size,
                              self.block, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
                              DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32)
-        self._at8 = ctypes.addressof(self._c)    # (a name of its own: the two kinds of cache are not mistaken)
+        self._at8 = ctypes.addressof(self._c)    # (names of their own: one kind of descriptor is not taken for another)
 
     def c(self) -> _KvCacheQ8:
         return self._c
@@ -747,10 +747,22 @@ class HeadNorm:
         c = _HeadNorm(_ptr(q_weight), _ptr(k_weight), eps, offset, int(per_head))
         self._c = _HeadNormShape(c, given[0][0].shape[-1] if given else 0,
                                  DTYPE_F32 if given and given[0][0].dtype == torch.float32 else DTYPE_BF16, *heads)
-        self._at = ctypes.addressof(self._c)
+        self._at_norm = ctypes.addressof(self._c)
 
     def c(self) -> _HeadNorm:
         return self._c.norm
+
+
+class WrongKind(ValueError, AttributeError):
+    """An argument is a descriptor of another kind (an AttributeError too: calls raised that before)."""
+
+
+def _wrong_kind(**given) -> WrongKind:
+    """name=(argument, kind): the error for the first argument that is not of its kind."""
+    for name, (x, kind) in given.items():
+        if not isinstance(x, kind):
+            return WrongKind(f"{name} must be a {kind.__name__}, not a {type(x).__name__}")
+    return WrongKind(f"{', '.join(given)}: incomplete")
 
 
 def moe_attention_workspace_bytes(T: int, heads: int, cache: KvCache) -> int:
@@ -782,7 +794,11 @@ def moe_kv_append(q, k, v, rope, positions, slots, cache: KvCache, q_out, worksp
     q and k/v: [T][heads][head_dim] and [T][kv_heads][head_dim], any distances
     between tokens and heads that are multiples of 16 bytes; rope: the table
     of moe_rope_table, or None (no rotation); q and q_out may both be None."""
-    st = (_fast or _load_binding()).kv_append(q, k, v, rope, positions, slots, cache._at, q_out, workspace, interleaved, stream)
+    try:
+        at = cache._at
+    except AttributeError:
+        raise _wrong_kind(cache=(cache, KvCache)) from None
+    st = (_fast or _load_binding()).kv_append(q, k, v, rope, positions, slots, at, q_out, workspace, interleaved, stream)
     if st:
         _check(st, "moe_kv_append")
     return q_out
@@ -792,8 +808,12 @@ def moe_kv_append_norm(q, k, v, rope, positions, slots, norm: HeadNorm, cache: K
                        interleaved: bool = False, stream=None):
     """moe_kv_append with norms of queries and keys, each head by itself, before
     the rotation."""
-    st = (_fast or _load_binding()).kv_append_norm(q, k, v, rope, positions, slots, norm._at, cache._at, q_out, workspace,
-                                                   interleaved, stream)
+    try:
+        norm_at, at = norm._at_norm, cache._at
+    except AttributeError:
+        raise _wrong_kind(norm=(norm, HeadNorm), cache=(cache, KvCache)) from None
+    st = (_fast or _load_binding()).kv_append_norm(q, k, v, rope, positions, slots, norm_at, at, q_out, workspace, interleaved,
+                                                   stream)
     if st:
         _check(st, "moe_kv_append_norm")
     return q_out
@@ -804,8 +824,12 @@ def moe_kv_append_q8(q, k, v, rope, positions, slots, norm: HeadNorm | None, cac
     """moe_kv_append into a cache in 8 bits, with norms (None: without).  A
     block's rows are written in order; the call that writes the first of them
     begins the block anew.  Tokens of the same block follow one another."""
-    st = (_fast or _load_binding()).kv_append_q8(q, k, v, rope, positions, slots, norm and norm._at, cache._at8, q_out,
-                                                 workspace, interleaved, stream)
+    try:
+        norm_at, at = None if norm is None else norm._at_norm, cache._at8
+    except AttributeError:
+        raise _wrong_kind(**({} if norm is None else {"norm": (norm, HeadNorm)}), cache=(cache, KvCacheQ8)) from None
+    st = (_fast or _load_binding()).kv_append_q8(q, k, v, rope, positions, slots, norm_at, at, q_out, workspace, interleaved,
+                                                 stream)
     if st:
         _check(st, "moe_kv_append_q8")
     return q_out
@@ -814,7 +838,11 @@ def moe_kv_append_q8(q, k, v, rope, positions, slots, norm: HeadNorm | None, cac
 def moe_kv_read_q8(slots, cache: KvCacheQ8, k_out, v_out, workspace: torch.Tensor, stream=None):
     """Rows slots [T] of a cache in 8 bits, into k_out and v_out [T][kv_heads]
     [head_dim] of its dtype (one of them may be None)."""
-    st = (_fast or _load_binding()).kv_read_q8(slots, cache._at8, k_out, v_out, workspace, stream)
+    try:
+        at = cache._at8
+    except AttributeError:
+        raise _wrong_kind(cache=(cache, KvCacheQ8)) from None
+    st = (_fast or _load_binding()).kv_read_q8(slots, at, k_out, v_out, workspace, stream)
     if st:
         _check(st, "moe_kv_read_q8")
     return k_out, v_out
@@ -843,7 +871,11 @@ def moe_tree_attention(q, q_offsets, ctx_len, mask, cache: KvCache, out, lse, wo
     [words] int32 bits) allows (None: the token itself and those before it).
     scale: 1 / sqrt(head_dim) by default.  lse may be None.  A cache whose page
     table has about as many rows as requests that take part serves best."""
-    st = (_fast or _load_binding()).tree_attention(q, q_offsets, ctx_len, mask, cache._at, out, lse, workspace, scale, stream)
+    try:
+        at = cache._at
+    except AttributeError:
+        raise _wrong_kind(cache=(cache, KvCache)) from None
+    st = (_fast or _load_binding()).tree_attention(q, q_offsets, ctx_len, mask, at, out, lse, workspace, scale, stream)
     if st:
         _check(st, "moe_tree_attention")
     return out
@@ -852,7 +884,11 @@ def moe_tree_attention(q, q_offsets, ctx_len, mask, cache: KvCache, out, lse, wo
 def moe_tree_attention_q8(q, q_offsets, ctx_len, mask, cache: KvCacheQ8, out, lse, workspace: torch.Tensor,
                           scale: float | None = None, stream=None):
     """moe_tree_attention over a cache in 8 bits; q and out are of its dtype."""
-    st = (_fast or _load_binding()).tree_attention_q8(q, q_offsets, ctx_len, mask, cache._at8, out, lse, workspace, scale,
+    try:
+        at = cache._at8
+    except AttributeError:
+        raise _wrong_kind(cache=(cache, KvCacheQ8)) from None
+    st = (_fast or _load_binding()).tree_attention_q8(q, q_offsets, ctx_len, mask, at, out, lse, workspace, scale,
                                                       stream)
     if st:
         _check(st, "moe_tree_attention_q8")
