@@ -9,10 +9,10 @@
 //   q = qs (q0 + q1 / 2^4): qs a power of two for a unit's rows, so that the
 //       largest component lies in 224..448; a bf16 component has 8 significant
 //       bits, an e4m3 number 4, so two of them hold it exactly (but for what is
-//       2^-22 of the unit's largest);
+//       2^-21 of the unit's largest: half a step of 2^-13, beside 224 at least);
 //   w = w0 + w1 / 2^5 + w2 / 2^10: the weights of a tile, scaled so that each row's
-//       largest is 2^8: good to 2^-14 of a weight (2^-12: they come from f16), or to
-//       2^-28 of the row's largest in the tile.  (Scaled by one bound for the whole
+//       largest is 2^8: good to 2^-14 of a weight (and 2^-11 before that: they come
+//       from f16), or to 2^-28 of the row's largest in the tile.  (Scaled by one bound for the whole
 //       context, light weights behind a heavy one, which a long context has many
 //       of, kept few bits or none; so each tile's product is added up in registers.
 //       Values widened to f16, with f16 weights, cost more shared memory traffic

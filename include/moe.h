@@ -746,15 +746,17 @@ moe_status moe_kv_read_q8(const int64_t *slots, const moe_read_params *params, c
 /*
  * moe_tree_attention over a cache in 8 bits: arguments, limits, masks, flags
  * and results as there, with q and out of the cache's dtype and its keys and
- * values code * scale.  Scales of positions that are seen are finite and not
- * negative; those of values may count as 2^-64 below that.  What lies in
- * positions that a token does not see, their scales too, has no influence on it.
+ * values code * scale.  Scales of positions that are seen are 0 to 2^120 (the
+ * largest that an append begins a block with); those of values may count as
+ * 2^-64 below that.  What lies in positions that a token does not see, their
+ * scales too, has no influence on it.
  * Tensor cores (heads and pages as there): up to 64 rows a key head on average,
- * queries are taken exactly but for 2^-22 of the largest component of the rows
- * that are worked on together, and weights times values' scales are off by up to
- * 2^-12 of themselves or 2^-28 of the row's largest among 128 positions.  With
- * more rows, weights are rounded to bf16 (2^-8 of each, their sum is not), and
- * so are values whose scale is no power of two.
+ * queries are taken exactly but for 2^-21 of the largest component of the rows
+ * that are worked on together (up to 32 of a request and key head), and weights
+ * times values' scales are off by up to 2^-11 + 2^-14 of themselves and 2^-28 of
+ * the row's largest among 128 positions; the weights' sum is not.  With more
+ * rows, weights are rounded to bf16 (2^-8 of each, their sum is not), and so are
+ * values whose scale is no power of two.
  */
 size_t moe_attention_q8_workspace_bytes(int32_t T, int32_t heads, const moe_kv_cache_q8 *cache);
 
