@@ -61,3 +61,30 @@ def test_positions_of_skipped_tokens_are_checked_without_queries(T, block, skip,
             moe.moe_kv_append_norm(qs[0], k, v, rope, pos, slots, c.norm, plain, qs[1], ws)
             assert moe.moe_device_status(ws) == want
             c8.check(c, c.slots, True, c.wk)
+
+
+@pytest.mark.parametrize("T", [7, 64, 255, 256])
+@pytest.mark.parametrize("block", [1, 4, 16])
+@pytest.mark.parametrize("kind", ["singles", "drafts"])
+def test_padded_decode_batches(T, block, kind):
+    """Up to 256 tokens, some of them padding: between requests, inside blocks, at either end."""
+    g = torch.Generator().manual_seed(T + block)
+    if kind == "singles":
+        spans = [(int(torch.randint(0, 16, (1,), generator=g)), 1) for _ in range(T)]
+    else:
+        spans, left = [], T
+        while left:
+            n = min(left, int(torch.randint(1, 12, (1,), generator=g)))
+            spans.append((int(torch.randint(0, 16, (1,), generator=g)), n))
+            left -= n
+    c = append.Case(spans, 4, 2, 64, 64, 16, seed=T)
+    c.slots[torch.rand(T, generator=g) < 0.35] = -1
+    c.slots[0] = c.slots[T - 1] = -1
+    c8 = append.Cache8(c, block, 12)
+    q, k, v, rope, pos, slots = c.on_gpu()
+    q_out = torch.full((T, 4, 64), math.nan, dtype=c.dt, device=DEV)
+    ws = append.workspace()
+    moe.moe_kv_append_q8(q, k, v, rope, pos, slots, c.norm, c8.gpu, q_out, ws)
+    assert moe.moe_device_status(ws) == 0
+    append.close(q_out, *c.want(c.q, c.wq), c.dt)
+    c8.check(c, c.slots, True, c.wk)
