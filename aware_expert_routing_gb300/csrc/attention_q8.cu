@@ -481,7 +481,7 @@ attention_q8_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
 #pragma unroll
                     for (int p = C::kParts - 1; p >= 0; --p) {
                         uint32_t y[16];
-                        tmem_ld<16>(lanes + kOCol + (t & 1) * C::kNP + p * R + i0, y);
+                        tmem_ld16(lanes + kOCol + (t & 1) * C::kNP + p * R + i0, y);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] = p == C::kParts - 1 ? __uint_as_float(y[i]) : fmaf(x[i], 1.f / kPart, __uint_as_float(y[i]));
                     }
@@ -626,15 +626,15 @@ attention_q8_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h01) : "f"(x1), "f"(x0));
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h23) : "f"(x3), "f"(x2));
                         c0[y] = codes4(h01, h23, true);
-                        c1[y] = codes4(h01, h23, C::kParts > 2);
-                        if (C::kParts > 2) c2[y] = codes4(h01, h23, false);
+                        c1[y] = codes4(h01, h23, true);
+                        c2[y] = codes4(h01, h23, false);
                     }
                     auto put = [&](int part_, const uint32_t (&x)[4]) {
                         *reinterpret_cast<uint4*>(pk + ((((part_ * R + i0) >> 4) ^ pswz) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
                     };
                     put(0, c0);
                     put(1, c1);
-                    if (C::kParts > 2) put(2, c2);
+                    put(2, c2);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 // the product before this one, while this one's is under way

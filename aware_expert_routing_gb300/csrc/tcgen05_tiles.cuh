@@ -55,9 +55,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
-// 16 or 32 columns; 16 from two places at once.
-template <int kN> __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[kN]);
-template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 columns; 16 from two places at once.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
         "tcgen05.wait::ld.sync.aligned;"
@@ -65,7 +64,6 @@ template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t
         : "r"(taddr)
         : "memory");
 }
-template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 
 __device__ __forceinline__ void tmem_ld16_two(uint32_t t0, uint32_t t1, uint32_t (&r)[32]) {
     asm volatile(
