@@ -66,7 +66,8 @@
 // besides what the MMAs read.  A tree of 64 at 131000 180 us (0.75 PFLOP/s; 217
 // with eight warps on keys and values in turn and one row tile a unit, 202 with
 // the keys left in e4m3 and their scales multiplied into S by the softmax; 120 in
-// bf16), 16 trees of 16 to 4000 37 (27.5 in bf16).
+// bf16), 16 trees of 16 to 4000 38.6 (27.5 in bf16; 37.5 with an instruction for registers
+// in each of the warps' parts, which a warpgroup may not have).
 #include <cudaTypedefs.h>
 
 #include <cstddef>
@@ -314,272 +315,272 @@ attention_tc_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
 
     if (!any) {
         // no work for this CTA
-    } else if (warp == 0 || (kQ8 && (warp == 2 || warp == 3))) {
-        // ---- producer: pages into the ring, in the order in which the MMAs read them ----
-        // (8 bits: a warp each for keys, scales and values)
+    } else if (warp < C::kFirst) {
+        // ---- all but the softmax ----
+        // (Registers: one instruction for all warps of a warpgroup, whatever each of them does.)
         if (kQ8 || kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQ8 ? kLess : 120));
-        uint32_t seq = 0;
-        const int page = a.page_size;
-        const int per = page < kKeys ? kKeys / page : 1;        // pages of a tile
-        const int prow = page < kKeys ? page : kKeys;           // rows of a copy
-        const uint32_t bytes = (uint32_t)prow * D * (kQ8 ? 1 : 2);
-        const int batch = 32 / per;                             // tiles whose table entries the warp reads at once
-        const int my_tile = lane / per, my_page = lane - my_tile * per;
-        const int wide = page / kKeys;                          // tiles of a page of more than 128 rows
-        // This lane's page of the batch of tiles from j on of a part: is there
-        // one, its entry in the table, and its first 8-row group in the cache
-        // (-1: no page).
-        auto has = [&](const Walk& U, int j) {
-            return my_tile < batch && j + my_tile < U.nk && (U.kt + j + my_tile) * kKeys + my_page * prow < U.q.ctx + U.q.n;
-        };
-        auto read = [&](const Walk& U, int j) -> int {
-            const int t = U.kt + j + my_tile;
-            return has(U, j) ? a.page_table[(size_t)U.r * a.max_pages + (page <= kKeys ? t * per + my_page : t / wide)] : 0;
-        };
-        auto group_of = [&](int id, int j) -> int {
-            if (!has(W, j)) return -1;
-            if (id < 0 || id >= a.n_pages) {
-                raise_flag(a.flags, kFlagBadIndex);
-                id = 0;
-            }
-            const int row = page <= kKeys ? 0 : (W.kt + j + my_tile) % wide * kKeys;
-            const long long at = ((long long)id * a.kv_heads + W.h) * page + row;
-            return (int)(kQ8 ? at : at / 8);   // 8 bits: the row
-        };
-        const int vals = kQ8 && warp == 3 ? 1 : 0;
-        const uint32_t stages = !kQ8 ? C::kStages : vals ? C::kValStages : C::kKeyStages;
-        uint64_t *full = kQ8 ? S.raw_full[vals] : S.full, *empty = kQ8 ? S.raw_empty[vals] : S.empty;
-        unsigned char* to = !kQ8 ? ring : raw + vals * C::kKeyStages * C::kRaw;
-        auto load = [&](const CUtensorMap* map, int g) {
-            const uint32_t st = kQ8 ? seq % stages : seq % C::kStages, ph = (kQ8 ? seq / stages : seq / C::kStages) & 1;
-            wait_bar(&empty[st], ph ^ 1, S, a.flags);
-            ++seq;
-            const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
-            if (warp_aborted(S)) return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[st], n * bytes);
-                S.armed[vals] = seq;
-            }
-            __syncwarp();
-            if (g < 0) return;
-            if (kQ8) tma_rows(smem_u32(to + st * C::kRaw) + lane * bytes, map, g, &full[st]);
-            else tma_load_4d(smem_u32(to + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &full[st]);
-        };
-        ScaleCopy<C::kScaleStages> scales(a, prow, lane);
-        auto load_scales = [&](int cur, int at) {
-            wait_bar(&S.sc_empty[scales.stage()], scales.phase() ^ 1, S, a.flags);
-            scales.copy(a, cur, at, per, scale_ring, &S.sc_full[scales.stage()]);
-        };
-        int id0 = read(W, 0), id1 = read(W, batch);
-        bool more = true;
-        while (more) {
-            int g_prev = -1, at = 0, cur = group_of(id0, 0), nxt = id1;
-            Walk N = W;
-            for (int j = 0; j < W.nk; ++j) {
-                const int t = __shfl_sync(0xffffffffu, cur, min(31, at * per + lane));
-                const int g = lane < per ? t : -1;
-                if (kQ8) {
-                    if (warp == 2) load_scales(cur, at);
-                    else load(vals ? &map_v : &map_k, g);
-                } else {
-                    load(&map_k, g);
-                    if (kTiles == 2) load(&map_v, g);
-                    else if (j > 0) load(&map_v, g_prev);
+        if (warp == 0 || (kQ8 && (warp == 2 || warp == 3))) {
+            // ---- producer: pages into the ring, in the order in which the MMAs read them ----
+            // (8 bits: a warp each for keys, scales and values)
+            uint32_t seq = 0;
+            const int page = a.page_size;
+            const int per = page < kKeys ? kKeys / page : 1;        // pages of a tile
+            const int prow = page < kKeys ? page : kKeys;           // rows of a copy
+            const uint32_t bytes = (uint32_t)prow * D * (kQ8 ? 1 : 2);
+            const int batch = 32 / per;                             // tiles whose table entries the warp reads at once
+            const int my_tile = lane / per, my_page = lane - my_tile * per;
+            const int wide = page / kKeys;                          // tiles of a page of more than 128 rows
+            // This lane's page of the batch of tiles from j on of a part: is there
+            // one, its entry in the table, and its first 8-row group in the cache
+            // (-1: no page).
+            auto has = [&](const Walk& U, int j) {
+                return my_tile < batch && j + my_tile < U.nk && (U.kt + j + my_tile) * kKeys + my_page * prow < U.q.ctx + U.q.n;
+            };
+            auto read = [&](const Walk& U, int j) -> int {
+                const int t = U.kt + j + my_tile;
+                return has(U, j) ? a.page_table[(size_t)U.r * a.max_pages + (page <= kKeys ? t * per + my_page : t / wide)] : 0;
+            };
+            auto group_of = [&](int id, int j) -> int {
+                if (!has(W, j)) return -1;
+                if (id < 0 || id >= a.n_pages) {
+                    raise_flag(a.flags, kFlagBadIndex);
+                    id = 0;
                 }
-                if (j == 0) {   // the next part's first entries, while this part is loaded
-                    more = N.next(a);
-                    if (more) {
-                        id0 = read(N, 0);
-                        id1 = read(N, batch);
+                const int row = page <= kKeys ? 0 : (W.kt + j + my_tile) % wide * kKeys;
+                const long long at = ((long long)id * a.kv_heads + W.h) * page + row;
+                return (int)(kQ8 ? at : at / 8);   // 8 bits: the row
+            };
+            const int vals = kQ8 && warp == 3 ? 1 : 0;
+            const uint32_t stages = !kQ8 ? C::kStages : vals ? C::kValStages : C::kKeyStages;
+            uint64_t *full = kQ8 ? S.raw_full[vals] : S.full, *empty = kQ8 ? S.raw_empty[vals] : S.empty;
+            unsigned char* to = !kQ8 ? ring : raw + vals * C::kKeyStages * C::kRaw;
+            auto load = [&](const CUtensorMap* map, int g) {
+                const uint32_t st = kQ8 ? seq % stages : seq % C::kStages, ph = (kQ8 ? seq / stages : seq / C::kStages) & 1;
+                wait_bar(&empty[st], ph ^ 1, S, a.flags);
+                ++seq;
+                const int n = __popc(__ballot_sync(0xffffffffu, g >= 0));
+                if (warp_aborted(S)) return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[st], n * bytes);
+                    S.armed[vals] = seq;
+                }
+                __syncwarp();
+                if (g < 0) return;
+                if (kQ8) tma_rows(smem_u32(to + st * C::kRaw) + lane * bytes, map, g, &full[st]);
+                else tma_load_4d(smem_u32(to + st * C::kStage) + lane * bytes, map, 0, 0, 0, g, &full[st]);
+            };
+            ScaleCopy<C::kScaleStages> scales(a, prow, lane);
+            auto load_scales = [&](int cur, int at) {
+                wait_bar(&S.sc_empty[scales.stage()], scales.phase() ^ 1, S, a.flags);
+                scales.copy(a, cur, at, per, scale_ring, &S.sc_full[scales.stage()]);
+            };
+            int id0 = read(W, 0), id1 = read(W, batch);
+            bool more = true;
+            while (more) {
+                int g_prev = -1, at = 0, cur = group_of(id0, 0), nxt = id1;
+                Walk N = W;
+                for (int j = 0; j < W.nk; ++j) {
+                    const int t = __shfl_sync(0xffffffffu, cur, min(31, at * per + lane));
+                    const int g = lane < per ? t : -1;
+                    if (kQ8) {
+                        if (warp == 2) load_scales(cur, at);
+                        else load(vals ? &map_v : &map_k, g);
+                    } else {
+                        load(&map_k, g);
+                        if (kTiles == 2) load(&map_v, g);
+                        else if (j > 0) load(&map_v, g_prev);
+                    }
+                    if (j == 0) {   // the next part's first entries, while this part is loaded
+                        more = N.next(a);
+                        if (more) {
+                            id0 = read(N, 0);
+                            id1 = read(N, batch);
+                        }
+                    }
+                    g_prev = g;
+                    if (++at == batch) {
+                        at = 0;
+                        cur = group_of(nxt, j + 1);
+                        nxt = read(W, j + 1 + batch);
                     }
                 }
-                g_prev = g;
-                if (++at == batch) {
-                    at = 0;
-                    cur = group_of(nxt, j + 1);
-                    nxt = read(W, j + 1 + batch);
+                if (!kQ8 && kTiles == 1) load(&map_v, g_prev);
+                W = N;
+            }
+            if (kQ8) asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (warp == 1) {
+            // ---- MMA: one warp issues, in the order of the ring ----
+            constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
+            constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
+            const uint32_t ctl = uniform(smem_u32(&S)), ring0 = uniform(smem_u32(ring)), q0 = uniform(smem_u32(qs)), tm = uniform(tmem);
+            uint32_t st = 0, ph = 0;                        // next stage of the ring, its phase
+            uint32_t tile[2] = {0, 0}, seg[2] = {0, 0};     // per row tile: key tiles, units
+            // waits for the next stage; its shared memory address
+            auto stage_wait = [&](uint32_t s_, uint32_t p_) {
+                wait_bar(&S.full[s_], p_, S, a.flags);
+                tmem_fence_after_sync();
+                return ring0 + s_ * C::kStage;
+            };
+            auto advance = [&]() {
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
-            }
-            if (!kQ8 && kTiles == 1) load(&map_v, g_prev);
-            W = N;
-        }
-        if (kQ8) asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 1) {
-        // ---- MMA: one warp issues, in the order of the ring ----
-        if (kQ8 || kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQ8 ? kLess : 120));
-        constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsTile, kKeys);
-        constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsTile, D) | (1u << 16);   // V: MN-major
-        const uint32_t ctl = uniform(smem_u32(&S)), ring0 = uniform(smem_u32(ring)), q0 = uniform(smem_u32(qs)), tm = uniform(tmem);
-        uint32_t st = 0, ph = 0;                        // next stage of the ring, its phase
-        uint32_t tile[2] = {0, 0}, seg[2] = {0, 0};     // per row tile: key tiles, units
-        // waits for the next stage; its shared memory address
-        auto stage_wait = [&](uint32_t s_, uint32_t p_) {
-            wait_bar(&S.full[s_], p_, S, a.flags);
-            tmem_fence_after_sync();
-            return ring0 + s_ * C::kStage;
-        };
-        auto advance = [&]() {
-            if (++st == C::kStages) {
-                st = 0;
-                ph ^= 1;
-            }
-        };
-        // Shared-memory descriptors: a constant part, and the address in the
-        // low word.  Q and K are K-major, 8-row groups 1024 and kBlocks * 1024
-        // bytes apart.  V is MN-major: swizzle atoms of 8 keys by 64
-        // components, 1024 bytes apart along the components (leading offset)
-        // and kBlocks * 1024 along the keys (stride offset).
-        constexpr uint64_t q_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(1024 >> 4) << 32 | 1u << 16;
-        constexpr uint64_t k_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | 1u << 16;
-        constexpr uint64_t v_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | (1024u >> 4) << 16;
-        auto issue_s = [&](int w, uint32_t buf, uint32_t kaddr) {
-            const uint32_t qa = (q0 + w * C::kQTile) >> 4, ka = kaddr >> 4, d = tm + buf * 128;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_ss(d, q_hi | (qa + ((k / 4) * (kRowsTile * 128) + (k % 4) * 32) / 16),
-                       k_hi | (ka + ((k / 4) * 1024 + (k % 4) * 32) / 16), idesc_s, k > 0);
-            mma_commit(ctl + (uint32_t)offsetof(Control, s_full) + 8 * (buf));
-        };
-        // The product with V starts with the first 64 keys' P.
-        auto issue_pv = [&](int w, uint32_t buf, uint32_t pp, uint32_t vaddr, uint32_t acc) {
-            const uint32_t va = vaddr >> 4, d = tm + kOCol + w * D, p = tm + buf * 128;
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k) {
-                if (k == kKeys / 32) {
-                    wait_bar(&S.p_full[buf], pp, S, a.flags);
-                    tmem_fence_after_sync();
-                }
-                const uint32_t pk = p + (k / 4) * 64 + (k % 4) * 8;
-                const uint64_t vk = v_hi | (va + k * 2 * C::kBlocks * 1024 / 16);
-                mma_ts(d, pk, vk, idesc_o, k > 0 ? 1u : acc);
-                if (C::kLow) mma_ts(d, pk + 32, vk, idesc_o, 1u);
-            }
-            mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
-        };
-        // Once a wait has given up, all return at once: the loop then runs out on
-        // whatever the shared and tensor memory hold, which harms nothing.
-        // (Leaving it early costs a vote a tile: 3 % for a tree of 64 tokens.)
-        do {
-            const int nw = uniform(kTiles == 2 && rows_of(W, 1) > 0 ? 2 : 1);
-            const int n = uniform(W.nk);
-            if (kTiles == 1) {
-                wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
-                uint32_t kaddr = stage_wait(st, ph);
-                issue_s(0, tile[0] & 1, kaddr);
-                mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
-                advance();
-                for (int j = 0; j < n; ++j) {
-                    if (j + 1 < n) {
-                        kaddr = stage_wait(st, ph);
-                        issue_s(0, (tile[0] + 1) & 1, kaddr);
-                        mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
-                        advance();
+            };
+            // Shared-memory descriptors: a constant part, and the address in the
+            // low word.  Q and K are K-major, 8-row groups 1024 and kBlocks * 1024
+            // bytes apart.  V is MN-major: swizzle atoms of 8 keys by 64
+            // components, 1024 bytes apart along the components (leading offset)
+            // and kBlocks * 1024 along the keys (stride offset).
+            constexpr uint64_t q_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(1024 >> 4) << 32 | 1u << 16;
+            constexpr uint64_t k_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | 1u << 16;
+            constexpr uint64_t v_hi = (uint64_t)1 << 46 | (uint64_t)2 << 61 | (uint64_t)(C::kBlocks * 1024 >> 4) << 32 | (1024u >> 4) << 16;
+            auto issue_s = [&](int w, uint32_t buf, uint32_t kaddr) {
+                const uint32_t qa = (q0 + w * C::kQTile) >> 4, ka = kaddr >> 4, d = tm + buf * 128;
+    #pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(d, q_hi | (qa + ((k / 4) * (kRowsTile * 128) + (k % 4) * 32) / 16),
+                           k_hi | (ka + ((k / 4) * 1024 + (k % 4) * 32) / 16), idesc_s, k > 0);
+                mma_commit(ctl + (uint32_t)offsetof(Control, s_full) + 8 * (buf));
+            };
+            // The product with V starts with the first 64 keys' P.
+            auto issue_pv = [&](int w, uint32_t buf, uint32_t pp, uint32_t vaddr, uint32_t acc) {
+                const uint32_t va = vaddr >> 4, d = tm + kOCol + w * D, p = tm + buf * 128;
+    #pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k) {
+                    if (k == kKeys / 32) {
+                        wait_bar(&S.p_full[buf], pp, S, a.flags);
+                        tmem_fence_after_sync();
                     }
-                    const uint32_t buf = tile[0] & 1;
-                    const uint32_t pp = (tile[0] >> 1) & 1;
-                    wait_bar(&S.p_half[buf], pp, S, a.flags);
-                    const uint32_t vaddr = stage_wait(st, ph);
-                    issue_pv(0, buf, pp, vaddr, j > 0);
+                    const uint32_t pk = p + (k / 4) * 64 + (k % 4) * 8;
+                    const uint64_t vk = v_hi | (va + k * 2 * C::kBlocks * 1024 / 16);
+                    mma_ts(d, pk, vk, idesc_o, k > 0 ? 1u : acc);
+                    if (C::kLow) mma_ts(d, pk + 32, vk, idesc_o, 1u);
+                }
+                mma_commit(ctl + (uint32_t)offsetof(Control, pv_done) + 8 * (kTiles == 1 ? buf : (uint32_t)w));
+            };
+            // Once a wait has given up, all return at once: the loop then runs out on
+            // whatever the shared and tensor memory hold, which harms nothing.
+            // (Leaving it early costs a vote a tile: 3 % for a tree of 64 tokens.)
+            do {
+                const int nw = uniform(kTiles == 2 && rows_of(W, 1) > 0 ? 2 : 1);
+                const int n = uniform(W.nk);
+                if (kTiles == 1) {
+                    wait_bar(&S.q_full[0], seg[0]++ & 1, S, a.flags);
+                    uint32_t kaddr = stage_wait(st, ph);
+                    issue_s(0, tile[0] & 1, kaddr);
                     mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
                     advance();
-                    ++tile[0];
-                }
-            } else {
-                uint32_t kaddr = stage_wait(st, ph);
-                for (int w = 0; w < nw; ++w) {
-                    wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
-                    issue_s(w, w, kaddr);
-                }
-                mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
-                advance();
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t v_st = st, v_ph = ph;
-                    advance();
-                    uint32_t vaddr = 0;
-                    for (int w = 0; w < nw; ++w) {
-                        const uint32_t pp = tile[w] & 1;
-                        wait_bar(&S.p_half[w], pp, S, a.flags);
-                        ++tile[w];
-                        if (w == 0) vaddr = stage_wait(v_st, v_ph);
-                        tmem_fence_after_sync();
-                        issue_pv(w, w, pp, vaddr, j > 0);
-                        if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (v_st));
+                    for (int j = 0; j < n; ++j) {
                         if (j + 1 < n) {
-                            if (w == 0) kaddr = stage_wait(st, ph);
-                            issue_s(w, w, kaddr);
-                            if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                            kaddr = stage_wait(st, ph);
+                            issue_s(0, (tile[0] + 1) & 1, kaddr);
+                            mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                            advance();
+                        }
+                        const uint32_t buf = tile[0] & 1;
+                        const uint32_t pp = (tile[0] >> 1) & 1;
+                        wait_bar(&S.p_half[buf], pp, S, a.flags);
+                        const uint32_t vaddr = stage_wait(st, ph);
+                        issue_pv(0, buf, pp, vaddr, j > 0);
+                        mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                        advance();
+                        ++tile[0];
+                    }
+                } else {
+                    uint32_t kaddr = stage_wait(st, ph);
+                    for (int w = 0; w < nw; ++w) {
+                        wait_bar(&S.q_full[w], seg[w]++ & 1, S, a.flags);
+                        issue_s(w, w, kaddr);
+                    }
+                    mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                    advance();
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t v_st = st, v_ph = ph;
+                        advance();
+                        uint32_t vaddr = 0;
+                        for (int w = 0; w < nw; ++w) {
+                            const uint32_t pp = tile[w] & 1;
+                            wait_bar(&S.p_half[w], pp, S, a.flags);
+                            ++tile[w];
+                            if (w == 0) vaddr = stage_wait(v_st, v_ph);
+                            tmem_fence_after_sync();
+                            issue_pv(w, w, pp, vaddr, j > 0);
+                            if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (v_st));
+                            if (j + 1 < n) {
+                                if (w == 0) kaddr = stage_wait(st, ph);
+                                issue_s(w, w, kaddr);
+                                if (w == nw - 1) mma_commit(ctl + (uint32_t)offsetof(Control, empty) + 8 * (st));
+                            }
+                        }
+                        if (j + 1 < n) advance();
+                    }
+                }
+            } while (W.next(a));
+        } else if (kQ8 && warp >= 4) {
+            // ---- 8 bits: tiles to bf16; a warpgroup the keys, one the values; thread = key ----
+            // A code times a power of two is exact in bf16.  What a scale has besides one
+            // (which no append writes) is multiplied into the scores for keys; values are
+            // rounded to bf16 with it.
+            const int v = (warp - 4) / 4, key = threadIdx.x & 127, swz = D == 128 ? key & 7 : key >> 1 & 3;
+            const uint32_t stages = v ? C::kValStages : C::kKeyStages;
+            const unsigned char* rows = raw + v * C::kKeyStages * C::kRaw + key * D;
+            unsigned char* const to = ring + (key >> 3) * (C::kBlocks * 1024) + (key & 7) * 128;
+            constexpr int kAtOnce = kTiles == 1 ? D / 16 : 2;   // (few registers)
+            uint32_t tile = 0, seq0 = 0;
+            do {
+                for (int j = 0; j < W.nk; ++j, ++tile) {
+                    // (its place in the ring, which the MMAs read in the order K0 K1 V0 K2 V1 ..., with two row tiles K0 V0 K1 V1 ...)
+                    const uint32_t seq = seq0 + (kTiles == 2 ? 2 * j + v : v ? j == W.nk - 1 ? 2 * j + 1 : 2 * j + 2 : j == 0 ? 0 : 2 * j - 1);
+                    const uint32_t sst = tile % C::kScaleStages, st = seq % C::kStages, rst = tile % stages;
+                    wait_bar(&S.sc_full[sst], (tile / C::kScaleStages) & 1, S, a.flags);
+                    float f = scale_ring[(sst * 2 + v) * kKeys + key];
+                    wait_bar(&S.raw_full[v][rst], (tile / stages) & 1, S, a.flags);
+                    const unsigned char* from = rows + rst * C::kRaw;
+                    wait_bar(&S.empty[st], ((seq / C::kStages) & 1) ^ 1, S, a.flags);
+                    if (v == 0) {
+                        // (From here on the softmax of the tile four before has read its own: this
+                        // place in the ring was that of a later tile's keys or values, whose product came
+                        // after its weights.)
+                        const uint32_t bits = __float_as_uint(f);
+                        const float p = __uint_as_float(bits & 0xff800000u);
+                        const bool odd = (bits & 0x7fffffu) != 0 && p != 0.f && fabsf(p) < INFINITY;
+                        odd_part[sst * kKeys + key] = odd ? __uint_as_float((bits & 0x7fffffu) | 0x3f800000u) : 1.f;
+                        const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                        if (lane == 0) S.odd[sst][warp & 3] = word;
+                        f = p;
+                    }
+    #pragma unroll
+                    for (int x0 = 0; x0 < D / 16; x0 += kAtOnce) {
+                        uint4 c[kAtOnce];
+    #pragma unroll
+                        for (int x = 0; x < kAtOnce; ++x) c[x] = *reinterpret_cast<const uint4*>(from + ((x0 + x ^ swz) << 4));
+                        if (x0 + kAtOnce == D / 16) {
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(&S.raw_empty[v][rst]);
+                                mbar_arrive(&S.sc_empty[sst]);
+                            }
+                        }
+    #pragma unroll
+                        for (int x = 0; x < kAtOnce; ++x) {
+                            const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+                            uint32_t y[8];
+    #pragma unroll
+                            for (int z = 0; z < 8; ++z) y[z] = scaled2(w[z >> 1] >> (z & 1) * 16, f);
+                            const int ch = 2 * (x0 + x);   // 16-byte pieces of the row in bf16
+                            unsigned char* at = to + st * C::kStage + (ch >> 3) * 1024;
+                            *reinterpret_cast<uint4*>(at + (((ch & 7) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(at + (((ch & 7) + 1 ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
                     }
-                    if (j + 1 < n) advance();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.full[st]);
                 }
-            }
-        } while (W.next(a));
-    } else if (kQ8 && warp < C::kFirst) {
-        // ---- 8 bits: tiles to bf16; a warpgroup the keys, one the values; thread = key ----
-        // A code times a power of two is exact in bf16.  What a scale has besides one
-        // (which no append writes) is multiplied into the scores for keys; values are
-        // rounded to bf16 with it.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLess));
-        const int v = (warp - 4) / 4, key = threadIdx.x & 127, swz = D == 128 ? key & 7 : key >> 1 & 3;
-        const uint32_t stages = v ? C::kValStages : C::kKeyStages;
-        const unsigned char* rows = raw + v * C::kKeyStages * C::kRaw + key * D;
-        unsigned char* const to = ring + (key >> 3) * (C::kBlocks * 1024) + (key & 7) * 128;
-        constexpr int kAtOnce = kTiles == 1 ? D / 16 : 2;   // (few registers)
-        uint32_t tile = 0, seq0 = 0;
-        do {
-            for (int j = 0; j < W.nk; ++j, ++tile) {
-                // (its place in the ring, which the MMAs read in the order K0 K1 V0 K2 V1 ..., with two row tiles K0 V0 K1 V1 ...)
-                const uint32_t seq = seq0 + (kTiles == 2 ? 2 * j + v : v ? j == W.nk - 1 ? 2 * j + 1 : 2 * j + 2 : j == 0 ? 0 : 2 * j - 1);
-                const uint32_t sst = tile % C::kScaleStages, st = seq % C::kStages, rst = tile % stages;
-                wait_bar(&S.sc_full[sst], (tile / C::kScaleStages) & 1, S, a.flags);
-                float f = scale_ring[(sst * 2 + v) * kKeys + key];
-                wait_bar(&S.raw_full[v][rst], (tile / stages) & 1, S, a.flags);
-                const unsigned char* from = rows + rst * C::kRaw;
-                wait_bar(&S.empty[st], ((seq / C::kStages) & 1) ^ 1, S, a.flags);
-                if (v == 0) {
-                    // (From here on the softmax of the tile four before has read its own: this
-                    // place in the ring was that of a later tile's keys or values, whose product came
-                    // after its weights.)
-                    const uint32_t bits = __float_as_uint(f);
-                    const float p = __uint_as_float(bits & 0xff800000u);
-                    const bool odd = (bits & 0x7fffffu) != 0 && p != 0.f && fabsf(p) < INFINITY;
-                    odd_part[sst * kKeys + key] = odd ? __uint_as_float((bits & 0x7fffffu) | 0x3f800000u) : 1.f;
-                    const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                    if (lane == 0) S.odd[sst][warp & 3] = word;
-                    f = p;
-                }
-#pragma unroll
-                for (int x0 = 0; x0 < D / 16; x0 += kAtOnce) {
-                    uint4 c[kAtOnce];
-#pragma unroll
-                    for (int x = 0; x < kAtOnce; ++x) c[x] = *reinterpret_cast<const uint4*>(from + ((x0 + x ^ swz) << 4));
-                    if (x0 + kAtOnce == D / 16) {
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&S.raw_empty[v][rst]);
-                            mbar_arrive(&S.sc_empty[sst]);
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < kAtOnce; ++x) {
-                        const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
-                        uint32_t y[8];
-#pragma unroll
-                        for (int z = 0; z < 8; ++z) y[z] = scaled2(w[z >> 1] >> (z & 1) * 16, f);
-                        const int ch = 2 * (x0 + x);   // 16-byte pieces of the row in bf16
-                        unsigned char* at = to + st * C::kStage + (ch >> 3) * 1024;
-                        *reinterpret_cast<uint4*>(at + (((ch & 7) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4*>(at + (((ch & 7) + 1 ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.full[st]);
-            }
-            seq0 += 2 * W.nk;
-        } while (W.next(a));
-    } else if (warp < C::kFirst) {
-        if (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+                seq0 += 2 * W.nk;
+            } while (W.next(a));
+        }
     } else {
         // ---- softmax: warpgroup w owns row tile w, thread = row = TMEM lane ----
         // registers: 384 x 168 at launch = 128 x 120 + 256 x 192
