@@ -316,8 +316,8 @@ __device__ __forceinline__ void weigh(const Lane<T, kMode>& L, uint64_t (&z)[Vec
 // Bounded by the bytes, and nearly as much by the instructions (two thirds of all
 // issue slots): a thread keeps its two words' angles for all rows of the token
 // that it goes through, and works on pairs of components.  16000 tokens with 32 + 2
-// x 4 heads of 128: 61 us, 5.5 TB/s (50 at the copy rate); with single components
-// and divisions for places 76.
+// x 4 heads of 128: 60 us, 5.6 TB/s (50 at the copy rate; fp32 106 of 99); with single
+// components and divisions for places 76.
 template <typename T, int kMode, bool kCache>
 __device__ __forceinline__ void plain_rows(const NormArgs& n, float* scratch, int t, int y, int thread, int threads) {
     constexpr int N = Vec<T>::kN;
@@ -457,11 +457,14 @@ __device__ __forceinline__ uint32_t most_bits(const uint64_t (&z)[N], bool finit
 //
 // What takes the time is a chain: slots and positions around the chunk; the
 // search; rows, angles and the scale; their maximum over the warps; codes.  256
-// drafted tokens wait for little else (8.3 us; their bytes would take 1.4).  Of
+// drafted tokens wait for little else (8.1 us; their bytes would take 1.4).  Of
 // a prompt many such chains have to be under way, and each has to be short: with one
 // warp for all of a block's rows of one head 16000 tokens took 112 us, with four
 // 106, with the search shared by eight heads 93, with one round of rows at a time
-// (registers) 81, fewer instructions 75; 48 for the bytes.
+// (registers) 81, fewer instructions 74; 48 for the bytes.  The registers that so many
+// thread blocks leave do not hold everything: of bf16 72 bytes are written to and 56
+// read from local memory a thread (rotations that are not on words 240 and 204).  fp32:
+// 16000 117 us of 92, with a scale for every row (bf16) 63.
 constexpr int kWarps = 4;
 constexpr int kStash = 4;       // rounds of a warp that shared memory holds: 8 KB in bf16
 constexpr int kSkipped = 256;   // a token this far behind the last of its block still belongs to it
@@ -736,7 +739,10 @@ __device__ __forceinline__ void block_rows(const NormArgs& n, unsigned char* sme
     }
 }
 
-constexpr int kBounds = 7;   // thread blocks on an SM, 72 registers: 16000 tokens 81 us; 6 86, 8 87
+// Thread blocks on an SM.  6 / 7 (72 registers) / 8: 16000 tokens of a prompt 78.6 / 75.0 /
+// 72.2 us, 4000 23.6 / 22.0 / 21.9, 1000 9.9 / 11.0 / 11.8, 256 drafted ones of 16 requests
+// 8.9 / 9.5 / 9.9, 1000 single ones 43 / 31 / 31.
+constexpr int kBounds = 7;
 
 // kMany: small thread blocks, many on an SM (16000 tokens with 14 of them 61 us, 12 66, 18 68).
 template <typename T, int kMode, bool kMany>
@@ -767,19 +773,27 @@ __global__ void __launch_bounds__(32 * kWarps, kBounds) append_q8_kernel(const N
 }
 
 // A thread block takes up to eight heads' keys or values, which share the search
-// for blocks, as long as there are about as many thread blocks as run at once:
-// 16000 tokens 93 us (then), with four 96, two 103, one 106; 4000 44 with eight, 25
-// with one.
+// for blocks, as long as there are about as many thread blocks as run at once.  Up to
+// 8 / 4 / 2 / 1: 16000 tokens 75.0 / 77.6 / 81.8 / 90.1 us, 4000 22.0 / 22.1 / 22.0 / 23.9
+// (44.7 with eight whatever their number).
 constexpr int kTeamHeads = 8, kTeams = 1000;
-// From so many tokens on small thread blocks append to a bf16 or fp32 cache: 1000
-// tokens 8.2 us, 16000 61 (of 256 threads 10.8, 169); below, large ones: 400 6.1
-// (6.5), 600 6.4 (7.6).
-constexpr int kManyNorm = 800;
-// Up to so many tokens a token's rows are spread over thread blocks, a row a thread,
-// into a cache in 8 bits and else: 100 tokens 3.1 us (in one thread block each 3.6),
-// 200 4.9 (3.7); in 8 bits, where those for keys and values run beside them, 200 of
-// single requests 10.7 (13.3).
-constexpr int kSpread8 = 304, kSpread = 128;
+// The three forms of the append to a bf16 or fp32 cache: a token's rows spread over thread
+// blocks, a row a thread, up to kSpread tokens; a thread block of 256 threads a token; small
+// ones from kManyNorm on.  Tokens, spread / 256 threads / small, us:
+//   32 + 2 x 4 heads of 128  100 3.1 / 3.3 / 4.9, 128 3.0 / 3.6 / 5.0, 200 4.7 / 3.7 / 5.0,
+//                            304 5.0 / 3.6 / 5.0, 400 7.7 / 6.7 / 6.0, 600 10.7 / 7.9 / 7.2,
+//                            800 14.4 / 10.7 / 8.2, 1000 17.2 / 13.4 / 8.2, 4000 63 / 43 / 17
+//   8 + 2 x 1 of 128         200 2.9 / 2.9 / 3.4, 400 4.5 / 4.5 / 3.6, 800 6.4 / 6.5 / 4.6
+//   32 + 2 x 4 of 256        100 3.1 / 3.9 / 7.4, 200 5.8 / 4.9 / 8.6, 400 10.9 / 8.9 / 9.5,
+//                            600 15.5 / 9.8 / 11.1, 800 19.8 / 13.3 / 13.1
+// (304 tokens are all on the SMs at once in blocks of 256 threads, 400 are not.)  A number
+// of tokens alone is a coarse border: between 400 and 800 it costs up to 40 % with few heads.
+constexpr int kManyNorm = 800, kSpread = 128;
+// The same for the queries beside a cache in 8 bits, where thread blocks for keys and values
+// run with them: two tokens a thread block above.  Spread / two, us: single tokens 64 6.0 /
+// 7.5, 200 11.3 / 14.1, 304 16.7 / 17.2, 600 28.0 / 27.8, 1000 31.4 / 30.8; of a prompt 200 6.7
+// / 6.6, 600 8.4 / 8.5.
+constexpr int kSpread8 = 304;
 
 template <typename T, bool kQ8>
 cudaError_t launch_append_norm(NormArgs n, cudaStream_t s) {
@@ -799,8 +813,13 @@ cudaError_t launch_append_norm(NormArgs n, cudaStream_t s) {
     size_t smem = n.smem_scratch;
     if (kQ8) {
         // Few tokens may lie in a block each, which a search takes one after the other; many
-        // are mostly a request's: 256 / 1000 tokens of as many requests 12 / 29 us (1000 one by
-        // one 43), of one request 7 / 10 (20).
+        // are mostly a request's.  A stretch of 1 / 4 / a block's 16 tokens, us: as many requests
+        // 256 11.0 / 16.2 / 50, 257 11.0 / 16.1 / 50, 1000 29.0 / 30.8 / 55, 1025 29.7 / 31.3 / 55,
+        // 4000 97 / 95 / 108; two tokens a request 1024 24.7 / 22.9 / 35.8, 2048 44 / 42 / 41; eight
+        // 512 15.2 / 11.6 / 16.9, 2048 28.9 / 27.6 / 24.1; one request 256 7.6 / 6.0 / 8.0, 1000 24.4
+        // / 10.9 / 10.5, 1025 24.5 / 10.9 / 10.6, 4000 32.8 / 29.9 / 21.8.  (What counts is how many
+        // blocks begin in a stretch, which the host does not know: single tokens cost up to 1.7
+        // times more just past a border.)
         n.chunk = n.block == 1 ? kWarps * (32 / n.G) : a.T <= 256 ? 1 : a.T <= 1024 ? 4 : n.block < 32 ? n.block : 32;
         const long long chunks = ((long long)a.T + n.chunk - 1) / n.chunk;
         n.team_heads = (int)std::max(1LL, std::min((long long)std::min(kTeamHeads, 2 * a.kv_heads), chunks * 2 * a.kv_heads / kTeams));
@@ -839,7 +858,8 @@ cudaError_t launch_append_norm(NormArgs n, cudaStream_t s) {
 
 // ---- reading back -------------------------------------------------------------------
 // Bounded by the bytes: 131000 tokens of 4 heads of 128 take 63 us, 6.4 TB/s (with
-// each thread working out its tokens' places 88, two thirds of it instructions).
+// each thread working out its tokens' places 88, two thirds of it instructions), to fp32
+// 104 of 100.
 // A thread block has some tokens, whose places it works out once; a thread 16 bytes of the result in kReadTokens of them at a time, all of
 // whose codes are on their way at once.
 struct ReadArgs {
@@ -854,8 +874,11 @@ struct ReadArgs {
 };
 
 constexpr int kReadTokens = 4;
-// A thread block's tokens, where they are many: 131000 63.1 us, 65000 33.5 (with four
-// 66.2, 34.6); below, four: 16000 8.8, 4000 4.1 (with sixteen 9.4, 4.8).
+// A thread block's tokens: sixteen where they are many, else four.  Four / sixteen, us: 4
+// key heads of 128 4000 4.6 / 5.5, 16000 10.6 / 11.6, 32000 18.0 / 18.3, 48000 25.6 / 25.3,
+// 65000 33.8 / 32.9; to fp32 16000 16.4 / 18.0, 24000 23.2 / 22.3, 65000 58.4 / 53.7; 8 of 256
+// 32000 63.5 / 64.4, 48000 93.9 / 92.7; 1 of 128, whose thread blocks are smaller, 4000 2.4 /
+// 2.4, 16000 5.8 / 4.6, 32000 8.6 / 7.0, 65000 16.8 / 10.7.
 constexpr int kReadMany = 16;
 constexpr int kManyRead = 32768;
 

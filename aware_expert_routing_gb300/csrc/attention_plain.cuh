@@ -3,6 +3,11 @@
 // in 8 bits (attention_q8.cu), whose codes are exact in bf16: they become bf16 on
 // their way into shared memory, and the scales go into the scores and, with the
 // weights, into the products with V.
+//
+// A cache in 8 bits, 64 single tokens up to 8000 positions with 32 + 4 heads: bf16, heads
+// of 80 253 us (the bytes 24), of 192 537 (59), of 256 673 (78), of 128 with pages of 24
+// positions 284 (39); fp32, heads of 128 282 (56), and 16 trees of 16 up to 4000 334, of which
+// the products take 119 at the FMA rate.
 #pragma once
 
 #include <cuda_fp16.h>

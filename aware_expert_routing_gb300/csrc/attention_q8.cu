@@ -530,7 +530,7 @@ attention_q8_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap m
                 uint64_t u[kC / 2];   // in pairs of rows
                 const uint64_t ca2 = pack2(ca, ca), lg2 = pack2(lg, lg), inv2 = pack2(inv, inv), part = pack2(0.0625f, 0.0625f);
 #pragma unroll
-                for (int i0 = 0; i0 < kC; i0 += 16) {   // (32 at once spilled)
+                for (int i0 = 0; i0 < kC; i0 += 16) {   // (32 at once spilled more)
                     uint32_t h[32];
                     tmem_ld16_two(lanes + buf * C::kNS + i0, lanes + buf * C::kNS + R + i0, h);
 #pragma unroll
@@ -759,9 +759,13 @@ cudaError_t launch_q8_r(const AttentionArgs& a, long long rows, const CUtensorMa
 }  // namespace
 
 // Most rows a key head, on average, that this file's kernel takes, in units of 16
-// or 32; with more it reads the keys of a request three times.  Here / widened to
-// bf16: 64 requests of 3 tokens with 8 rows each to 8000 97 / 171 us, of 6 144 / 173, of
-// 8 163 / 173; 16 of 6 to 4000 28.1 / 33.6, of 8 33.0 / 34.5; 8 at 65000 43 / 55.
+// or 32; with more it reads the keys of a request three times.  Here / widened to bf16 /
+// a cache in bf16, us: 64 requests of 2 tokens with 8 rows each to 8000 56 / - / 90, of 3 88 /
+// 169 / 91, of 4 90 / 166 / 93, of 5 169 / 170 / -, of 6 172 / 171 / 95, of 8 171 / 176 / 96; 16 of
+// 2 to 4000 17.8 / - / 23.9, of 3 23.7 / 35.6 / -, of 4 24.7 / 35.0 / 24.0, of 6 34.5 / 36.1 / -,
+// of 8 34.8 / 37.0 / 25.7; one of 4 at 65000 33.7 / 46.9 / 37.0, of 8 43.4 / 54.2 / 44.9.  So from 33
+// rows on a cache in 8 bits saves memory, and time only over one long context.  (Units of 32
+// rows write 154 bytes a thread to local memory and read 108, those of 16 none with heads of 128.)
 constexpr int kFewRows = 64;
 
 cudaError_t launch_attention_q8(const AttentionArgs& a, bool bf16, bool tiles, int sms, cudaStream_t s) {

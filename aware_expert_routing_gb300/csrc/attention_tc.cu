@@ -63,11 +63,14 @@
 // rest is as above, without shares.  Half of the bytes come from HBM, but every
 // tile costs about 1500 cycles a warpgroup of conversions, which share the issue
 // slots with the softmax, and 64 KB written to shared memory and read from it
-// besides what the MMAs read.  A tree of 64 at 131000 180 us (0.75 PFLOP/s; 217
+// besides what the MMAs read.  A tree of 64 at 131000 184 us (0.75 PFLOP/s; 217
 // with eight warps on keys and values in turn and one row tile a unit, 202 with
-// the keys left in e4m3 and their scales multiplied into S by the softmax; 120 in
-// bf16), 16 trees of 16 to 4000 38.6 (27.5 in bf16; 37.5 with an instruction for registers
-// in each of the warps' parts, which a warpgroup may not have).
+// the keys left in e4m3 and their scales multiplied into S by the softmax; 112 to
+// 122 in bf16), 16 trees of 16 to 4000 38.2 (27.5 in bf16; 37.5 with an instruction for
+// registers in each of the warps' parts, which a warpgroup may not have), a prompt's
+// 2000 tokens at 8000 585 (309), 500 at 32000 366 (204).  With two row tiles a thread's
+// registers do not hold everything: 688 bytes are written to local memory and 518 read
+// (bf16: 4 and 12), a part of the issue slots that this costs.
 #include <cudaTypedefs.h>
 
 #include <cstddef>
