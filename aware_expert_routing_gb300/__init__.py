@@ -99,7 +99,15 @@ class _HeadNorm(ctypes.Structure):
 
 
 class _HeadNormShape(ctypes.Structure):     # csrc/binding.cpp: Norm
-    _fields_ = [("norm", _HeadNorm)] + [(n, ctypes.c_int32) for n in ("head_dim", "dtype", "q_heads", "k_heads")]
+    _fields_ = [("norm", _HeadNorm)] + [(n, ctypes.c_int32) for n in ("head_dim", "dtype", "q_heads", "k_heads", "device")]
+
+
+class _KvCacheOn(ctypes.Structure):         # csrc/binding.cpp: OnDevice
+    _fields_ = [("cache", _KvCache), ("device", ctypes.c_int32)]
+
+
+class _KvCacheQ8On(ctypes.Structure):
+    _fields_ = [("cache", _KvCacheQ8), ("device", ctypes.c_int32)]
 
 
 class _Read(ctypes.Structure):
@@ -324,6 +332,14 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} is required")
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+
+
+def _one_device(*tensors) -> int:
+    """The CUDA device that all of them (Nones left out) are on; -1: there is none."""
+    on = {t.device.index for t in tensors if t is not None}
+    if len(on) > 1:
+        raise ValueError(f"the tensors are on more than one device: {sorted(on)}")
+    return on.pop() if on else -1
 
 
 def moe_route(hidden, w_router, router_bias, params: RouteParams, routing: Routing,
@@ -666,13 +682,14 @@ class KvCache:
         self.n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.n_requests, self.max_pages = page_table.shape if page_table is not None else (0, 0)
         self.dtype = k.dtype
-        self._c = _KvCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr() if page_table is not None else None,
-                           self.n_pages, self.page_size, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
-                           DTYPE_BF16 if k.dtype == torch.bfloat16 else DTYPE_F32)
+        self._c = _KvCacheOn(_KvCache(
+            k.data_ptr(), v.data_ptr(), page_table.data_ptr() if page_table is not None else None, self.n_pages,
+            self.page_size, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
+            DTYPE_BF16 if k.dtype == torch.bfloat16 else DTYPE_F32), _one_device(k, v, page_table))
         self._at = ctypes.addressof(self._c)
 
     def c(self) -> _KvCache:
-        return self._c
+        return self._c.cache
 
 
 class KvCacheQ8:
@@ -705,14 +722,15 @@ class KvCacheQ8:
         self.block = self.page_size // k_scale.shape[2]
         self.n_requests, self.max_pages = page_table.shape if page_table is not None else (0, 0)
         self.dtype = dtype
-        self._c = _KvCacheQ8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                             page_table.data_ptr() if page_table is not None else None, self.n_pages, self.page_size,
-                             self.block, self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
-                             DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32)
+        self._c = _KvCacheQ8On(_KvCacheQ8(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr() if page_table is not None else None, self.n_pages, self.page_size, self.block,
+            self.kv_heads, self.head_dim, self.n_requests, self.max_pages,
+            DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32), _one_device(k, v, k_scale, v_scale, page_table))
         self._at8 = ctypes.addressof(self._c)    # (names of their own: one kind of descriptor is not taken for another)
 
     def c(self) -> _KvCacheQ8:
-        return self._c
+        return self._c.cache
 
 
 def alloc_kv_cache_q8(n_pages: int, kv_heads: int, page_size: int, head_dim: int, block: int, device,
@@ -746,7 +764,8 @@ class HeadNorm:
         heads = [t.shape[0] if per_head and t is not None else 0 for t in (q_weight, k_weight)]
         c = _HeadNorm(_ptr(q_weight), _ptr(k_weight), eps, offset, int(per_head))
         self._c = _HeadNormShape(c, given[0][0].shape[-1] if given else 0,
-                                 DTYPE_F32 if given and given[0][0].dtype == torch.float32 else DTYPE_BF16, *heads)
+                                 DTYPE_F32 if given and given[0][0].dtype == torch.float32 else DTYPE_BF16, *heads,
+                                 _one_device(q_weight, k_weight))
         self._at_norm = ctypes.addressof(self._c)
 
     def c(self) -> _HeadNorm:

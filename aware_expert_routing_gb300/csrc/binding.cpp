@@ -8,6 +8,7 @@
 // returns the call's moe_status; the package raises MoeError for it.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -46,6 +47,15 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
+// The current device, of which a call's tensors have to be: the library launches there.
+// (A default stream does not say which device is meant.)  -1: not looked up in this call.
+thread_local int g_device = -1;
+
+void check_device(int device, const char* name) {
+    if (g_device < 0) g_device = c10::cuda::current_device();
+    if (device != g_device) refuse("%s is on cuda:%d, the current device is cuda:%d", name, device, g_device);
+}
+
 // A contiguous CUDA tensor of a type; null for None where that is allowed.
 const at::Tensor* dense(PyObject* o, at::ScalarType type, const char* name, bool none_ok = false) {
     if (o == Py_None) {
@@ -55,6 +65,7 @@ const at::Tensor* dense(PyObject* o, at::ScalarType type, const char* name, bool
     const at::Tensor& t = tensor(o, name);
     if (!t.is_cuda() || t.scalar_type() != type || !t.is_contiguous())
         refuse("%s must be a contiguous CUDA tensor of %s", name, type_name(type));
+    check_device(t.device().index(), name);
     return &t;
 }
 
@@ -65,6 +76,7 @@ const at::Tensor& rows(PyObject* o, at::ScalarType type, int64_t T, int64_t head
         refuse("%s must be a CUDA tensor (%lld, %lld, %lld) of %s", name, (long long)T, (long long)heads, (long long)D,
                type_name(type));
     if (t.stride(2) != 1) refuse("%s: the components of a head must be adjacent", name);
+    check_device(t.device().index(), name);
     return t;
 }
 
@@ -113,6 +125,7 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F&& f) {
         PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
         return nullptr;
     }
+    g_device = -1;
     try {
         return PyLong_FromLong((long)f(args));
     } catch (const Bad&) {
@@ -123,11 +136,17 @@ PyObject* guarded(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F&& f) {
     }
 }
 
+// A KvCache's or KvCacheQ8's struct: what the C ABI reads, and the tensors' device.
+template <typename T> struct OnDevice {
+    T cache;
+    int32_t device;
+};
+
 // What the calls read of a cache, in its type or in 8 bits.
 struct Cache {
     const moe_kv_cache* plain = nullptr;
     const moe_kv_cache_q8* q8 = nullptr;
-    int32_t kv_heads, head_dim, n_requests;
+    int32_t kv_heads, head_dim, n_requests, device;
     at::ScalarType type;   // of the tensors that are not in the cache
 };
 
@@ -135,14 +154,17 @@ Cache cache_of(PyObject* o, bool q8) {
     const void* p = PyLong_AsVoidPtr(o);
     if (PyErr_Occurred()) throw Bad{};
     Cache c;
-    auto fill = [&](auto* x) {
+    auto fill = [&](const auto* on) {
+        const auto* x = &on->cache;
         c.kv_heads = x->kv_heads;
         c.head_dim = x->head_dim;
         c.n_requests = x->n_requests;
+        c.device = on->device;
         c.type = x->dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : at::kFloat;
+        return x;
     };
-    if (q8) fill(c.q8 = static_cast<const moe_kv_cache_q8*>(p));
-    else fill(c.plain = static_cast<const moe_kv_cache*>(p));
+    if (q8) c.q8 = fill(static_cast<const OnDevice<moe_kv_cache_q8>*>(p));
+    else c.plain = fill(static_cast<const OnDevice<moe_kv_cache>*>(p));
     return c;
 }
 
@@ -151,6 +173,7 @@ struct Norm {
     moe_head_norm norm;
     int32_t head_dim, dtype;
     int32_t q_heads, k_heads;   // with per_head; 0: no weights
+    int32_t device;
 };
 
 enum AppendKind { kAppend, kAppendNorm, kAppendQ8 };
@@ -192,6 +215,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor* slots = dense(x[5], at::kLong, "slots");
         if (slots->numel() != T) refuse("slots must hold %lld values", (long long)T);
         const at::Tensor* ws = dense(a[8], at::kByte, "workspace");
+        check_device(c.device, "cache");
         p.T = narrow(T, "T");
         const int inter = PyObject_IsTrue(a[9]);
         if (inter < 0) throw Bad{};
@@ -207,6 +231,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
             if (PyErr_Occurred()) throw Bad{};
             const Norm* w = static_cast<const Norm*>(at);
             if (w->norm.q_weight || w->norm.k_weight) {
+                check_device(w->device, "norm");
                 if (w->head_dim != D || w->dtype != (dt == at::kBFloat16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32))
                     refuse("the norm's weights must hold %lld values of %s a head", (long long)D, type_name(dt));
                 if (w->norm.per_head && ((w->norm.q_weight && q && w->q_heads != p.heads) || (w->norm.k_weight && w->k_heads != K)))
@@ -249,6 +274,7 @@ PyObject* kv_read_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
             p.v_head = distance(*v, 1);
         }
         const at::Tensor* ws = dense(a[4], at::kByte, "workspace");
+        check_device(c.device, "cache");
         return moe_kv_read_q8(static_cast<const int64_t*>(ptr(slots)), &p, c.q8, const_cast<void*>(ptr(k)),
                               const_cast<void*>(ptr(v)), ws->data_ptr(), (size_t)ws->numel(), stream_of(a[5], *slots));
     });
@@ -281,6 +307,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             p.mask_words = narrow(mask->size(1), "mask_words");
         }
         const at::Tensor* ws = dense(a[7], at::kByte, "workspace");
+        check_device(c.device, "cache");
         p.T = narrow(T, "T");
         p.heads = narrow(H, "heads");
         if (a[8] == Py_None) {
