@@ -462,9 +462,9 @@ __device__ __forceinline__ uint32_t most_bits(const uint64_t (&z)[N], bool finit
 // warp for all of a block's rows of one head 16000 tokens took 112 us, with four
 // 106, with the search shared by eight heads 93, with one round of rows at a time
 // (registers) 81, fewer instructions 74; 48 for the bytes.  The registers that so many
-// thread blocks leave do not hold everything: of bf16 72 bytes are written to and 56
-// read from local memory a thread (rotations that are not on words 240 and 204).  fp32:
-// 16000 117 us of 92, with a scale for every row (bf16) 63.
+// thread blocks leave do not hold everything: 72 bytes of spill stores and 56 of loads in
+// bf16 (240 and 204 for rotations that are not on words).  fp32: 16000 117 us of 92; with a
+// scale for every row (bf16) 63.
 constexpr int kWarps = 4;
 constexpr int kStash = 4;       // rounds of a warp that shared memory holds: 8 KB in bf16
 constexpr int kSkipped = 256;   // a token this far behind the last of its block still belongs to it

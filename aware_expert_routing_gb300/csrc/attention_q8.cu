@@ -765,7 +765,7 @@ cudaError_t launch_q8_r(const AttentionArgs& a, long long rows, const CUtensorMa
 // 2 to 4000 17.8 / - / 23.9, of 3 23.7 / 35.6 / -, of 4 24.7 / 35.0 / 24.0, of 6 34.5 / 36.1 / -,
 // of 8 34.8 / 37.0 / 25.7; one of 4 at 65000 33.7 / 46.9 / 37.0, of 8 43.4 / 54.2 / 44.9.  So from 33
 // rows on a cache in 8 bits saves memory, and time only over one long context.  (Units of 32
-// rows write 154 bytes a thread to local memory and read 108, those of 16 none with heads of 128.)
+// rows have 154 bytes of spill stores and 108 of loads, those of 16 none with heads of 128.)
 constexpr int kFewRows = 64;
 
 cudaError_t launch_attention_q8(const AttentionArgs& a, bool bf16, bool tiles, int sms, cudaStream_t s) {

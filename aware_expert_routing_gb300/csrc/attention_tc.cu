@@ -69,8 +69,8 @@
 // 122 in bf16), 16 trees of 16 to 4000 38.2 (27.5 in bf16; 37.5 with an instruction for
 // registers in each of the warps' parts, which a warpgroup may not have), a prompt's
 // 2000 tokens at 8000 585 (309), 500 at 32000 366 (204).  With two row tiles a thread's
-// registers do not hold everything: 688 bytes are written to local memory and 518 read
-// (bf16: 4 and 12), a part of the issue slots that this costs.
+// registers do not hold everything: 688 bytes of spill stores and 518 of loads (bf16: 4
+// and 12) are a part of the issue slots that this costs.
 #include <cudaTypedefs.h>
 
 #include <cstddef>
